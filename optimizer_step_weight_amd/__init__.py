@@ -11,6 +11,9 @@ sizes, so a short buffer would be read out of bounds).
 Entry points (same names as the C ABI in include/forge.h, without the ``forge_`` prefix):
     wgrad_step, dgrad, linear_backward_step, wgrad_gemm, optimizer_step,
     step_scalars, device_check, version, build_id, status_string, last_error
+and, from layer.py (include/forge_layer.h):
+    rmsnorm, rmsnorm_backward, grouped_gemm, grouped_dgrad, grouped_wgrad, grouped_wgrad_step,
+    MultiStep
 """
 from __future__ import annotations
 
@@ -85,11 +88,12 @@ def _lib():
                   "forge_linear_backward_step_fused_noalloc", "forge_wgrad_gemm", "forge_optimizer_step",
                   "forge_step_scalars", "forge_device_check"):
             getattr(L, f).restype = st
-        from . import _build
+        from . import _build, layer
         built, want = L.forge_build_id().decode(), _build.source_hash()
         if built != want:
             raise ImportError(f"{LIB_PATH} was built from other sources (build id {built}, sources {want}); "
                               "rebuild it with __graft_entry__.build()")
+        layer._declare(L)
         _lib_handle = L
     return _lib_handle
 
@@ -327,3 +331,17 @@ forge_version = version
 forge_build_id = build_id
 forge_status_string = status_string
 forge_last_error = last_error
+
+
+# include/forge_layer.h (imported on first use: the module needs torch)
+_LAYER = ("rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace", "grouped_gemm", "grouped_dgrad", "grouped_wgrad",
+          "grouped_wgrad_step", "MultiStep", "forge_rmsnorm", "forge_rmsnorm_backward", "forge_grouped_gemm",
+          "forge_grouped_dgrad", "forge_grouped_wgrad", "forge_grouped_wgrad_step")
+
+
+def __getattr__(name: str):
+    if name in _LAYER:
+        from . import layer
+        globals().update({n: getattr(layer, n) for n in _LAYER})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,90 @@
+// forge_grouped_wgrad.h -- dW_e = dY_e^T X_e of every expert on the LDS-DMA path of
+// forge_mainloop2.h, the gradient stored in fp32 or consumed by the optimizer's epilogue.
+//
+// One workgroup of 4 waves takes a 256 x 128 tile of an expert's weight (128 x 128 for the last
+// rows where N is an odd multiple of 128) and contracts the group's rows alone: the operands'
+// buffer ranges begin at the group's first row and end with its last, so a ragged end reads as
+// zero and an empty group contracts nothing.  Two workgroups share a CU: with few rows a group a
+// tile is mostly epilogue (the weight, moments or gradient through memory), and one workgroup's
+// contraction runs beside the other's epilogue.  Experts follow each other in the launch, each
+// spread over all XCDs, so that a crowded expert does not hold up one XCD.
+#pragma once
+
+#include "forge_epilogue.h"
+#include "forge_grouped.h"
+
+namespace forge {
+namespace grp {
+
+struct WTile {
+  GemmArgs g;     // the group's operands
+  int n0, k0;     // origin in the expert's weight
+  int row0;       // the same row in the stacked weights
+  bool half;      // 128 x 128
+};
+
+// Tiles of one expert: full ones, then the half ones of the last 128 rows.
+__host__ __device__ inline int wgrad_tiles(int64_t N, int64_t K) {
+  return (int)((N / 256 + (N % 256 ? 1 : 0)) * (K / 128));
+}
+
+__device__ __forceinline__ void wgrad_tile(const GroupedWgradArgs& a, WTile& t) {
+  const int per = wgrad_tiles(a.N, a.K), e = (int)blockIdx.x / per, b = (int)blockIdx.x - e * per;
+  const int nbk = (int)(a.K / 128), full = (int)(a.N / 256) * nbk;
+  int start, len, nb, kb;
+  group_rows(a.ends, a.E, a.T, e, start, len);
+  t.g.X = static_cast<const uint16_t*>(a.X) + (int64_t)start * a.K;
+  t.g.dY = static_cast<const uint16_t*>(a.dY) + (int64_t)start * a.N;
+  t.g.x_scale = t.g.dy_scale = nullptr;
+  t.g.T = len;
+  t.g.N = a.N;
+  t.g.K = a.K;
+  t.half = b >= full;
+  if (t.half) {
+    nb = (int)(a.N / 256);
+    kb = b - full;
+  } else {
+    plan::tile_coords_at(b, (int)(a.N / 256), nbk, nb, kb);
+  }
+  t.n0 = nb * 256;
+  t.k0 = kb * 128;
+  t.row0 = e * (int)a.N + t.n0;
+}
+
+template <int ST, int OPT>
+__global__ __launch_bounds__(ml2::THREADS, kOcc2) void grouped_step_kernel(GroupedWgradArgs a, EpiArgs e) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kSmem2];
+  WTile t;
+  wgrad_tile(a, t);
+  float* st = reinterpret_cast<float*>(smem);
+  if (t.half) {
+    floatx4 acc[4][4];
+    ml2::contract<Pipe2H>(acc, smem, t.g, t.n0, t.k0);
+    tile_epilogue<OPT, FORGE_W_BF16, ST, 1, true>(t.g, e, smem, t.row0, t.k0,
+                                                  [&](int) { ml2::stage_acc_all(st, acc, 1.0f); });
+  } else {
+    floatx4 acc[8][4];
+    ml2::contract<Pipe2>(acc, smem, t.g, t.n0, t.k0);
+    tile_epilogue<OPT, FORGE_W_BF16, ST, 2, true>(t.g, e, smem, t.row0, t.k0,
+                                                  [&](int h) { ml2::stage_acc_half(st, acc, 1.0f, h); });
+  }
+}
+
+using GroupedStepFn = void (*)(GroupedWgradArgs, EpiArgs);
+// Instantiated per moment format in forge_grouped_{f32,q8,q8d}.hip.
+template <int ST>
+GroupedStepFn select_grouped_step(int opt) {
+  switch (opt) {
+#define FORGE_CASE(O) \
+  case O: return grouped_step_kernel<ST, O>;
+    FORGE_FOR_EACH_OPT(FORGE_CASE)
+#undef FORGE_CASE
+  }
+  return nullptr;
+}
+extern template GroupedStepFn select_grouped_step<FORGE_S_F32>(int);
+extern template GroupedStepFn select_grouped_step<FORGE_S_Q8>(int);
+extern template GroupedStepFn select_grouped_step<FORGE_S_Q8D>(int);
+
+}  // namespace grp
+}  // namespace forge

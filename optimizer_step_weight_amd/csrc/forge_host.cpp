@@ -13,11 +13,18 @@
 #include <string>
 
 #include "forge.h"
+#include "forge_host_common.h"
 #include "forge_internal.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace forge {
+namespace host {
+
+void clear_error() { g_last_error.clear(); }
+
 
 forge_status fail(forge_status s, const char* fmt, ...) {
   char buf[512];
@@ -51,11 +58,6 @@ bool rule_has_v(int32_t opt) {
          opt == FORGE_ADAGRAD;
 }
 
-struct Range {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi)
-  const char* name = "";
-};
-
 Range range_of(const void* p, int64_t bytes, const char* name) {
   Range r;
   r.lo = reinterpret_cast<uintptr_t>(p);
@@ -64,14 +66,9 @@ Range range_of(const void* p, int64_t bytes, const char* name) {
   return r;
 }
 
-bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 // Every tensor stays below 2^48 bytes, so the size products below (and the kernels' own
 // bounds, which are tighter) cannot overflow 64-bit arithmetic.
-constexpr int64_t kMaxBytes = int64_t(1) << 48;
+static constexpr int64_t kMaxBytes = int64_t(1) << 48;
 
 forge_status check_tensor(const forge_tensor* t, const char* name) {
   if (!t) return fail(FORGE_ERR_ARG, "%s is NULL", name);
@@ -92,7 +89,7 @@ forge_status check_tensor(const forge_tensor* t, const char* name) {
 int64_t bytes_of(const forge_tensor* t) { return t->rows * t->cols * dtype_size(t->dtype); }
 
 // device check, cached per device
-std::atomic<int> g_dev_ok[64];
+static std::atomic<int> g_dev_ok[64];
 
 forge_status device_ok() {
   int dev = 0;
@@ -107,8 +104,6 @@ forge_status to_status(int herr) {
   return fail(FORGE_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString((hipError_t)herr));
 }
 
-}  // namespace
-
 // ------------------------------------------------------------------ per-step scalars
 // fp64 -> fp32 for a per-step scalar; false if it is not finite in fp32.
 static bool to_f32(double x, float* out) {
@@ -117,7 +112,7 @@ static bool to_f32(double x, float* out) {
   return std::isfinite(*out);
 }
 
-static forge_status compute_scalars(int32_t opt, const forge_hyper* h, int64_t step, forge::OptScalars* out) {
+forge_status compute_scalars(int32_t opt, const forge_hyper* h, int64_t step, forge::OptScalars* out) {
   if (!h) return fail(FORGE_ERR_ARG, "hyper is NULL");
   if (opt < FORGE_ADAMW || opt > FORGE_SGD_MOMENTUM) return fail(FORGE_ERR_ARG, "unknown optimizer %d", (int)opt);
   if (step < 1) return fail(FORGE_ERR_ARG, "step must be >= 1 (got %lld)", (long long)step);
@@ -206,14 +201,9 @@ static forge_status compute_scalars(int32_t opt, const forge_hyper* h, int64_t s
 }
 
 // ------------------------------------------------------------------ shared validation of the step
-struct StepPlan {
-  int w_type = 0, s_type = 0;
-  forge::EpiArgs e{};
-};
-
-static forge_status validate_step_outputs(int64_t N, int64_t K, forge_tensor* W, forge_tensor* m, forge_tensor* v,
-                                          const forge_hyper* hyper, int32_t opt, int64_t step, uint64_t seed,
-                                          const forge_step_opts* opts, StepPlan* plan, Range* outs, int* n_outs) {
+forge_status validate_step_outputs(int64_t N, int64_t K, forge_tensor* W, forge_tensor* m, forge_tensor* v,
+                                   const forge_hyper* hyper, int32_t opt, int64_t step, uint64_t seed,
+                                   const forge_step_opts* opts, StepPlan* plan, Range* outs, int* n_outs) {
   forge_status st;
   if ((st = check_tensor(W, "W")) != FORGE_OK) return st;
   if (W->rows != N || W->cols != K)
@@ -286,6 +276,11 @@ static forge_status validate_step_outputs(int64_t N, int64_t K, forge_tensor* W,
   e.s = s;
   return FORGE_OK;
 }
+
+}  // namespace host
+}  // namespace forge
+
+using namespace forge::host;
 
 static forge_status validate_inputs(const forge_tensor* X, const forge_tensor* dY, int* in_type, forge::GemmArgs* g,
                                     Range* ins, int* n_ins) {

@@ -1,0 +1,289 @@
+"""Binding of include/forge_layer.h: the RMS norm with the residual's addition and an fp8 output, the
+products grouped by expert, and the optimizer's step over many tensors in one launch.
+
+As in the package's other calls, this is argument marshalling only: outputs are the caller's
+tensors, work is enqueued on the current stream (or `stream`), and every call raises if the
+library is not built.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import torch
+
+from . import (BF16, F32, FP8_E4M3, I8_B64, I8DYN_B64, U8_B64, U8DYN_B64, Hyper, StepOpts, Tensor, _check, _dyn,
+               _hyper, _lib, _opt, _opts, _ref, _stream, _tensor)
+
+SCALE_MODE = {"row": 0, "tensor": 1}
+_CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
+_SIZE = {F32: 4, BF16: 2, FP8_E4M3: 1}
+
+
+class _MultiTensor(ctypes.Structure):
+    _fields_ = [("W", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _MultiInfo(ctypes.Structure):
+    _fields_ = [("bytes", ctypes.c_int64), ("chunks", ctypes.c_int64), ("tensors", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("opt", ctypes.c_int32), ("m_dtype", ctypes.c_int32),
+                ("v_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def _declare(L) -> None:
+    """Argument types of the entry points (called once, when the library is loaded)."""
+    P = ctypes.POINTER
+    T, H, O = P(Tensor), P(Hyper), P(StepOpts)
+    st, i32, i64, u64, f32, vp = (ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float,
+                                  ctypes.c_void_p)
+    L.forge_rmsnorm.argtypes = [T, T, T, f32, T, T, i32, vp, vp, vp]
+    L.forge_rmsnorm_backward.argtypes = [T, T, T, T, vp, T, T, vp, i64, vp]
+    L.forge_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.forge_grouped_gemm.argtypes = [T, T, vp, i32, T, vp]
+    L.forge_grouped_dgrad.argtypes = [T, T, vp, i32, T, vp]
+    L.forge_grouped_wgrad.argtypes = [T, T, vp, i32, T, vp]
+    L.forge_grouped_wgrad_step.argtypes = [T, T, vp, i32, T, T, T, H, i32, i64, u64, O, vp]
+    L.forge_multi_table_bytes.argtypes = [P(_MultiTensor), i32]
+    L.forge_multi_pack.argtypes = [P(_MultiTensor), i32, i32, i32, i32, vp, i64, P(_MultiInfo)]
+    L.forge_multi_step.argtypes = [P(_MultiInfo), vp, H, i32, i64, vp, O, vp]
+    for f in ("forge_rmsnorm", "forge_rmsnorm_backward", "forge_grouped_gemm", "forge_grouped_dgrad",
+              "forge_grouped_wgrad", "forge_grouped_wgrad_step", "forge_multi_pack", "forge_multi_step"):
+        getattr(L, f).restype = st
+    for f in ("forge_rmsnorm_backward_workspace_bytes", "forge_multi_table_bytes"):
+        getattr(L, f).restype = i64
+
+
+def _here(t: torch.Tensor, what: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (got a {t.device} tensor)")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _mat(t: Optional[torch.Tensor], what: str, scale: Optional[torch.Tensor] = None, scales: int = 0):
+    """A descriptor of t as rows of its last dimension (1-D: one row), all leading dimensions
+    flattened.  scale: a float32 tensor of `scales` elements (fp8 only)."""
+    if t is None:
+        return None
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype}")
+    _here(t, what)
+    if t.dim() < 1 or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    cols = t.shape[-1]
+    rows = t.numel() // cols if cols else 0
+    if scale is not None:
+        if code != FP8_E4M3:
+            raise ValueError(f"{what}: a {t.dtype} tensor takes no scale")
+        _vec(scale, f"the scale of {what}", scales)
+    return Tensor(t.data_ptr(), code, rows, cols, cols, None if scale is None else scale.data_ptr())
+
+
+def _vec(t: torch.Tensor, what: str, n: int, dtype=torch.float32) -> int:
+    """Address of a contiguous vector of n elements."""
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements (got {t.dtype}, {t.numel()})")
+    _here(t, what)
+    return t.data_ptr()
+
+
+def rmsnorm(x, gain, y, *, residual=None, h=None, rstd=None, y_scale=None, amax=None, eps: float = 1e-6,
+            scale_mode: str = "row", stream=None) -> None:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain over the last dimension
+    (forge_rmsnorm).  y float32, bfloat16 or float8_e4m3fn; fp8 writes one scale per row to y_scale
+    (scale_mode="row") or reads the tensor's one scale from it (scale_mode="tensor").  rstd (per
+    row, float32) is what the backward pass takes; amax (one float32) is raised to max |y|."""
+    if scale_mode not in SCALE_MODE:
+        raise ValueError(f"scale_mode must be 'row' or 'tensor' (got {scale_mode!r})")
+    X = _mat(x, "x")
+    rows = X.rows
+    _check(_lib().forge_rmsnorm(
+        _ref(X), _ref(_mat(residual, "residual")), _ref(_mat(gain, "gain")), eps, _ref(_mat(h, "h")),
+        _ref(_mat(y, "y", y_scale, rows if scale_mode == "row" else 1)), SCALE_MODE[scale_mode],
+        None if rstd is None else _vec(rstd, "rstd", rows), None if amax is None else _vec(amax, "amax", 1),
+        _stream(stream)))
+
+
+def rmsnorm_backward_workspace(rows: int, width: int, device="cuda") -> torch.Tensor:
+    """A workspace for rmsnorm_backward of [rows, width] tensors."""
+    n = _lib().forge_rmsnorm_backward_workspace_bytes(int(rows), int(width))
+    if n < 0:
+        raise ValueError(f"no workspace for [{rows}, {width}]")
+    return torch.empty(n // 4, dtype=torch.float32, device=device)
+
+
+def rmsnorm_backward(dy, h, gain, rstd, dx, dgain=None, *, dh=None, workspace=None, stream=None) -> None:
+    """dx (of x and of residual; dh, the gradient arriving on h itself, is added) and dgain
+    (float32, overwritten) of rmsnorm (forge_rmsnorm_backward).  A workspace is allocated where
+    dgain is wanted and none is given."""
+    H = _mat(h, "h")
+    rows, width = H.rows, H.cols
+    if dgain is not None and workspace is None:
+        workspace = rmsnorm_backward_workspace(rows, width, h.device)
+    if workspace is not None:
+        _here(workspace, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _check(_lib().forge_rmsnorm_backward(
+        _ref(_mat(dy, "dy")), _ref(_mat(dh, "dh")), _ref(H), _ref(_mat(gain, "gain")), _vec(rstd, "rstd", rows),
+        _ref(_mat(dx, "dx")), _ref(_mat(dgain, "dgain")), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _groups(ends, W, what="W"):
+    """(address of ends, number of groups); W [groups, N, K] where it is given."""
+    n = ends.numel()
+    if W is not None and (W.dim() != 3 or W.shape[0] != n):
+        raise ValueError(f"{what} must be [experts, N, K] with one expert for each of the {n} ends "
+                         f"(got {tuple(W.shape)})")
+    return _vec(ends, "ends", n, torch.int32), n
+
+
+def grouped_gemm(X, W, ends, Y, *, x_scale=None, w_scale=None, stream=None) -> None:
+    """Y[t] = X[t] W[e]^T for the rows t of group e (forge_grouped_gemm).  X [T, K] sorted by expert,
+    W [E, N, K], ends [E] int32 on the device: the first row after each group.  bfloat16, or
+    float8_e4m3fn X and W with x_scale [T] and w_scale [E, N]; Y [T, N] bfloat16."""
+    at, n = _groups(ends, W)
+    _check(_lib().forge_grouped_gemm(_ref(_mat(X, "X", x_scale, X.numel() // X.shape[-1])),
+                                     _ref(_mat(W, "W", w_scale, n * W.shape[1])), at, n, _ref(_mat(Y, "Y")),
+                                     _stream(stream)))
+
+
+def grouped_dgrad(dY, W, ends, dX, *, stream=None) -> None:
+    """dX[t] = dY[t] W[e] for the rows t of group e (forge_grouped_dgrad)."""
+    at, n = _groups(ends, W)
+    _check(_lib().forge_grouped_dgrad(_ref(_mat(dY, "dY")), _ref(_mat(W, "W")), at, n, _ref(_mat(dX, "dX")),
+                                      _stream(stream)))
+
+
+def grouped_wgrad(X, dY, ends, dW, *, stream=None) -> None:
+    """dW[e] = dY_e^T X_e in float32 for every group (forge_grouped_wgrad)."""
+    at, n = _groups(ends, dW, "dW")
+    _check(_lib().forge_grouped_wgrad(_ref(_mat(X, "X")), _ref(_mat(dY, "dY")), at, n, _ref(_mat(dW, "dW")),
+                                      _stream(stream)))
+
+
+def grouped_wgrad_step(X, dY, ends, W, m=None, v=None, *, opt="adamw", hyper=None, step: int, seed: int,
+                       m_scale=None, v_scale=None, w_preround_out=None, sr=True, state_map="linear",
+                       stream=None) -> None:
+    """The fused step of every expert's weight: W [E, N, K], m, v updated in place from
+    dW[e] = dY_e^T X_e (forge_grouped_wgrad_step; arguments as wgrad_step)."""
+    at, n = _groups(ends, W)
+    dyn = _dyn(state_map)
+    flat = lambda t: None if t is None else t.view(-1, t.shape[-1])  # noqa: E731
+    _check(_lib().forge_grouped_wgrad_step(
+        _ref(_mat(X, "X")), _ref(_mat(dY, "dY")), at, n, _ref(_mat(W, "W")), _ref(_tensor(flat(m), m_scale, dyn)),
+        _ref(_tensor(flat(v), v_scale, dyn)), ctypes.byref(_hyper(hyper)), _opt(opt), int(step),
+        int(seed) & 0xFFFFFFFFFFFFFFFF, _ref(_opts(w_preround_out, sr, W)), _stream(stream)))
+
+
+class MultiStep:
+    """One optimizer step over many tensors in one launch (forge_multi_pack, forge_multi_step).
+
+    W, g: lists of contiguous float32 or bfloat16 tensors of any size (16-byte aligned).  m, v:
+    their moments, all float32, or all 8-bit (int8 m, uint8 v) with m_scale / v_scale lists of
+    ceil(n / 64) float32 block scales in the linear or dynamic map; None for a moment the rule does
+    not keep.  group: which of step()'s hyper-parameter sets (at most 8) each tensor takes
+    (default: all the first).  seed: stochastic-rounding key of each tensor (default: its index).
+
+    The plan holds its tensors and their addresses: gradients are to be written into the same
+    tensors before every step (or set_grads() called with others).
+    """
+
+    def __init__(self, W: Sequence, g: Sequence, m: Optional[Sequence] = None, v: Optional[Sequence] = None, *,
+                 m_scale: Optional[Sequence] = None, v_scale: Optional[Sequence] = None,
+                 group: Optional[Sequence[int]] = None, seed: Optional[Sequence[int]] = None, opt="adamw",
+                 state_map: str = "linear"):
+        self.opt, self._dyn = _opt(opt), _dyn(state_map)
+        n = len(W)
+        self._lists = {"W": list(W)}
+        for name, x in (("g", g), ("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale)):
+            if x is not None and len(x) != n:
+                raise ValueError(f"{name} has {len(x)} tensors, W has {n}")
+            self._lists[name] = None if x is None else list(x)
+        self.group = [0] * n if group is None else [int(x) for x in group]
+        self.seed = list(range(n)) if seed is None else [int(x) & 0xFFFFFFFFFFFFFFFF for x in seed]
+        if len(self.group) != n or len(self.seed) != n:
+            raise ValueError("group and seed take one entry for each tensor")
+        self._device = None
+        self._pack()
+
+    def set_grads(self, g: Sequence) -> None:
+        """Takes other gradient tensors (the table is packed and copied anew)."""
+        if len(g) != len(self._lists["W"]):
+            raise ValueError(f"g has {len(g)} tensors, W has {len(self._lists['W'])}")
+        self._lists["g"] = list(g)
+        self._pack()
+
+    def _pack(self) -> None:
+        L = self._lists
+        n = len(L["W"])
+        if L["g"] is None:
+            raise ValueError("g is None")
+        codes = {}
+        for name, eight, dyn8, lin8 in (("m", torch.int8, I8DYN_B64, I8_B64), ("v", torch.uint8, U8DYN_B64, U8_B64)):
+            kinds = {t.dtype for t in L[name]} if L[name] else set()
+            if kinds - {torch.float32, eight} or len(kinds) > 1:
+                raise TypeError(f"{name}: all float32 or all {eight} (got {sorted(map(str, kinds))})")
+            codes[name] = F32 if not kinds or torch.float32 in kinds else (dyn8 if self._dyn else lin8)
+            if L[name + "_scale"] is not None and codes[name] == F32 and n:
+                raise ValueError(f"float32 {name} takes no scales")
+            if L[name + "_scale"] is None and codes[name] != F32:
+                raise ValueError(f"8-bit {name} needs {name}_scale")
+        entries = (_MultiTensor * n)()
+        for i, w in enumerate(L["W"]):
+            count = w.numel()
+            e = entries[i]
+            e.n, e.seed, e.group = count, self.seed[i], self.group[i]
+            for name in ("W", "g", "m", "v"):
+                if L[name] is None:
+                    continue
+                t = L[name][i]
+                if name in ("W", "g") and t.dtype not in (torch.float32, torch.bfloat16):
+                    raise TypeError(f"{name}[{i}]: unsupported dtype {t.dtype}")
+                setattr(e, name, _vec(t, f"{name}[{i}]", count, t.dtype) or None)
+            e.w_dtype, e.g_dtype = _CODE[w.dtype], _CODE[L["g"][i].dtype]
+            for name in ("m_scale", "v_scale"):
+                if L[name] is not None:
+                    setattr(e, name, _vec(L[name][i], f"{name}[{i}]", -(-count // 64)) or None)
+        lib = _lib()
+        size = lib.forge_multi_table_bytes(entries, n)
+        host = torch.empty(max(size, 16), dtype=torch.uint8)
+        self._info = _MultiInfo()
+        _check(lib.forge_multi_pack(entries, n, self.opt, codes["m"], codes["v"], host.data_ptr(), host.numel(),
+                                    ctypes.byref(self._info)))
+        self._hypers = (Hyper * 8)()
+        if n:
+            self._device = L["W"][0].device
+            self._table = host.to(self._device)   # a synchronous copy: the table is there for any stream
+
+    def step(self, *, step: int, hyper=None, grad_scale: Optional[torch.Tensor] = None, sr: bool = True,
+             stream=None) -> None:
+        """One step: hyper is one set of hyper-parameters, or a list with one for each group;
+        grad_scale one float32 on the device that multiplies every gradient."""
+        hypers = list(hyper) if isinstance(hyper, (list, tuple)) else [hyper if hyper is not None else {}]
+        if len(hypers) > 8:
+            raise ValueError("at most 8 groups of hyper-parameters")
+        for i, h in enumerate(hypers):
+            self._hypers[i] = _hyper(h)
+        if self._device is not None and self._device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {self._device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        opts = None if sr else StepOpts(None, 0)
+        _check(_lib().forge_multi_step(
+            ctypes.byref(self._info), self._table.data_ptr() if self._device is not None else None, self._hypers,
+            len(hypers), int(step), None if grad_scale is None else _vec(grad_scale, "grad_scale", 1), _ref(opts),
+            _stream(stream)))
+
+
+# the C ABI names
+forge_rmsnorm = rmsnorm
+forge_rmsnorm_backward = rmsnorm_backward
+forge_grouped_gemm = grouped_gemm
+forge_grouped_dgrad = grouped_dgrad
+forge_grouped_wgrad = grouped_wgrad
+forge_grouped_wgrad_step = grouped_wgrad_step

@@ -1,0 +1,498 @@
+"""The operators of include/forge_layer.h on the GPU against their definitions in 64 bits, at the
+sizes and values where they can go wrong.  Tolerances count roundings: u = 2^-24 for one fp32
+operation, half a step of the stored type for the last one, and a sum of n terms is off by at
+most its longest chain of additions times u times the sum of magnitudes."""
+import math
+
+import pytest
+import torch
+
+from tests import layer_ref as R
+
+pytestmark = pytest.mark.gpu
+BF, F32, FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24, FP8: 2.0 ** -4}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import optimizer_step_weight_amd as forge
+    forge.device_check(0)
+    return forge
+
+
+@pytest.fixture(autouse=True)
+def _name(request):
+    print("[case]", request.node.name, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def near(got, want, tol):
+    """|got - want| <= tol element by element (64-bit CPU tensors)."""
+    bad = (got.cpu().to(R.F64) - want).abs() - tol
+    assert not torch.isnan(bad).any() and float(bad.max()) <= 0, f"over by {float(bad.max())}"
+
+
+def chain(D):
+    """Longest chain of additions of a row's sum, with room for the rounding of each product, the
+    mean, the square root and the division."""
+    return -(-D // 64) + 40
+
+
+# ------------------------------------------------------------------ RMS norm
+WIDTHS = [1, 7, 8, 130, 512, 520, 1024, 2048, 2056, 4096, 5120, 6152, 8192, 8200, 16384, 16392]
+
+
+def norm_case(T, D, dt, seed):
+    g = gen(seed)
+    x, r = torch.randn(T, D, generator=g).to(dt), (3 * torch.randn(T, D, generator=g)).to(dt)
+    gain = 1 + 0.3 * torch.randn(D, generator=g)
+    if T > 2:
+        x[1] = 0
+        r[1] = 0                            # a row of zeros
+        x[2] *= 1e-18                       # squares that vanish beside eps
+        r[2] = 0
+    return x, r, gain
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("res", [True, False])
+def test_norm_forward(lib, D, dt, res):
+    eps = 1e-5
+    for T in (1, 5, 67):
+        x, r, gain = norm_case(T, D, dt, D + T)
+        gain = gain.to(BF) if T == 5 else gain
+        h = R.norm_h(x, r if res else None)
+        want, rstd = R.norm(h, gain, eps)
+        xd, rd, gd = x.cuda(), r.cuda() if res else None, gain.cuda()
+        hd = torch.full_like(xd, float("nan")) if res else None
+        tol = chain(D) * R.U
+        for out in (F32, BF, FP8):
+            y = torch.empty(T, D, dtype=out, device="cuda")
+            s, sc, am = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.zeros(1, device="cuda")
+            lib.rmsnorm(xd, gd, y, residual=rd, h=hd, rstd=s, y_scale=sc if out is FP8 else None, amax=am, eps=eps)
+            if res:
+                assert torch.equal(hd.cpu(), h)
+            near(s, rstd, tol * rstd)
+            near(am, want.abs().max().view(1), tol * want.abs().max())
+            if out is not FP8:
+                near(y, want, (tol + HALF[out]) * want.abs() + 2.0 ** -133)
+                continue
+            scale = want.abs().amax(1) / 448
+            near(sc, scale.clamp(min=2.0 ** -126), (tol + R.U) * scale + 2.0 ** -140)
+            got = y.cpu().to(R.F64) * sc.cpu().to(R.F64)[:, None]
+            # half a step of e4m3, of its smallest step 2^-9 below 2^-6, and two fp32 roundings
+            near(got, want, (HALF[FP8] + tol + 3 * R.U) * want.abs() + 2.0 ** -10 * sc.cpu().to(R.F64)[:, None])
+
+
+@pytest.mark.parametrize("D", [64, 100, 4096])
+def test_norm_tensor_scale(lib, D):
+    x, _, gain = norm_case(9, D, BF, D)
+    want, _ = R.norm(x, gain, 1e-6)
+    scale = torch.tensor([float(want.abs().max()) / 300], device="cuda")   # the largest values stay in range
+    small = scale / 100                                                     # and here they clamp to 448
+    for s in (scale, small):
+        y = torch.empty(9, D, dtype=FP8, device="cuda")
+        lib.rmsnorm(x.cuda(), gain.cuda(), y, y_scale=s, scale_mode="tensor")
+        s64 = float(s.cpu().to(R.F64))
+        w = (want / s64).clamp(-448, 448)
+        near(y, w, (HALF[FP8] + (chain(D) + 3) * R.U) * w.abs() + 2.0 ** -10)
+
+
+def test_norm_nan_and_infinity(lib):
+    """A bad element spoils its own row only, and amax keeps a NaN."""
+    for D in (4096, 100):
+        x, _, gain = norm_case(6, D, BF, 5)
+        x[3, D - 1], x[5, 0] = float("nan"), float("inf")
+        want, _ = R.norm(x, gain, 1e-6)
+        y, sc = torch.empty(6, D, dtype=FP8, device="cuda"), torch.empty(6, device="cuda")
+        am = torch.zeros(1, device="cuda")
+        lib.rmsnorm(x.cuda(), gain.cuda(), y, y_scale=sc, amax=am)
+        v = y.cpu().float() * sc.cpu()[:, None]
+        assert torch.isnan(v[3]).all() and torch.isnan(sc[3]) and torch.isnan(am).all()
+        assert torch.isnan(v[5, 0]) and torch.isfinite(v[[0, 1, 2, 4]]).all()
+        y = torch.empty(6, D, dtype=F32, device="cuda")
+        lib.rmsnorm(x.cuda(), gain.cuda(), y)
+        assert torch.isnan(y[3]).all() and torch.isnan(y[5, 0]) and bool((y[5, 1:] == 0).all())
+        assert torch.isfinite(y[[0, 1, 2, 4]]).all()
+
+
+def test_norm_in_place_and_other_stream(lib):
+    x, r, gain = norm_case(300, 1024, BF, 9)
+    h = R.norm_h(x, r)
+    want, _ = R.norm(h, gain, 1e-6)
+    for alias in ("x", "residual"):
+        xd, rd, y = x.cuda(), r.cuda(), torch.empty(300, 1024, dtype=BF, device="cuda")
+        gd = gain.cuda()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            lib.rmsnorm(xd, gd, y, residual=rd, h=xd if alias == "x" else rd)
+        s.synchronize()
+        assert torch.equal((xd if alias == "x" else rd).cpu(), h)
+        near(y, want, (chain(1024) * R.U + HALF[BF]) * want.abs() + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("with_dh", [True, False])
+def test_norm_backward(lib, D, dt, with_dh):
+    for T in (0, 1, 3, 67, 1500):
+        if T == 1500 and D > 4096:
+            continue
+        x, _, gain = norm_case(T, D, dt, D + T + 1)
+        g = gen(T)
+        dy, dh = torch.randn(T, D, generator=g).to(dt), torch.randn(T, D, generator=g).to(dt)
+        gain = gain.to(BF) if T == 3 else gain
+        rstd = R.norm(x, gain, 1e-5)[1].float()
+        dx, dgain = R.norm_grads(dy, x, gain, rstd, dh if with_dh else None)
+        a, s, hh = (dy.to(R.F64) * gain.to(R.F64)).abs(), rstd.to(R.F64)[:, None], x.to(R.F64).abs()
+        mag = s * a + hh * s ** 3 * (a * hh).mean(1, keepdim=True) + (dh.to(R.F64).abs() if with_dh else 0)
+        ws = lib.rmsnorm_backward_workspace(T, D)
+        ws.fill_(float("nan"))
+        outs = []
+        for want_gain in (True, True, False):
+            o, og = torch.empty(T, D, dtype=dt, device="cuda"), torch.full((D,), float("nan"), device="cuda")
+            lib.rmsnorm_backward(dy.cuda(), x.cuda(), gain.cuda(), rstd.cuda(), o, og if want_gain else None,
+                                 dh=dh.cuda() if with_dh else None, workspace=ws if want_gain else None)
+            near(o, dx, (chain(D) + 6) * R.U * mag + HALF[dt] * dx.abs() + 2.0 ** -133) if T else None
+            outs.append((o, og))
+        # rows of a group in a chain (two at most here), then the groups: 16 chains and their sum
+        n = -(-T // 1024) + 1024 // 16 + 16 + 4
+        near(outs[0][1], dgain, n * R.U * (dy.to(R.F64).abs() * hh * s).sum(0) + 2.0 ** -140)
+        assert torch.equal(outs[0][1], outs[1][1]) and torch.equal(outs[0][0], outs[2][0])
+        assert T == 0 or torch.isnan(outs[2][1]).all()   # not written where it is not wanted
+
+
+def test_norm_backward_in_place(lib):
+    x, _, gain = norm_case(40, 2048, BF, 2)
+    dy, dh = torch.randn(40, 2048, generator=gen(1)).to(BF), torch.randn(40, 2048, generator=gen(2)).to(BF)
+    rstd = R.norm(x, gain, 1e-6)[1].float()
+    dev = [t.cuda() for t in (dy, x, gain, rstd)]
+    want = torch.empty_like(dev[0])
+    lib.rmsnorm_backward(*dev, want, dh=dh.cuda())
+    a, b = dy.cuda(), dh.cuda()
+    lib.rmsnorm_backward(a, *dev[1:], a, dh=dh.cuda())
+    lib.rmsnorm_backward(*dev, b, dh=b)
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
+# ------------------------------------------------------------------ products grouped by expert
+def ints(shape, lim, seed, dt=BF):
+    return torch.randint(-lim, lim + 1, shape, generator=gen(seed)).to(dt)
+
+
+GROUPS = [
+    # ends, T
+    ([1], 1), ([0], 3), ([0, 0, 5], 5), ([17, 17, 40, 41, 41, 90], 90),
+    ([300, 300, 300, 301, 900, 1000], 1003),           # rows past the last end
+    ([64, 128, 192, 256], 256), ([63, 129, 191, 257], 257), ([2000, 2000, 2037], 2037),
+    (list(range(3, 3 * 131, 3)), 400),                 # 130 experts: three scans of 64
+    ([128 * i for i in range(1, 65)], 8192),           # 64 experts: the group after them in a scan of its own
+]
+
+
+@pytest.mark.parametrize("case", range(len(GROUPS)))
+@pytest.mark.parametrize("N,K", [(128, 128), (384, 256), (256, 640)])
+def test_grouped_products_exact(lib, case, N, K):
+    """Small integers: every sum is exact in fp32, so each output is the exact one rounded once."""
+    ends, T = GROUPS[case]
+    E = len(ends)
+    X, dY, W = ints((T, K), 4, 1), ints((T, N), 4, 2), ints((E, N, K), 4, 3)
+    ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    Xd, Dd, Wd = X.cuda(), dY.cuda(), W.cuda()
+    Y, dX = torch.full((T, N), float("nan"), dtype=BF, device="cuda"), torch.full((T, K), float("nan"), dtype=BF, device="cuda")
+    lib.grouped_gemm(Xd, Wd, ed, Y)
+    assert torch.equal(Y.cpu(), R.grouped(X, W, ends, True)[0].to(BF))
+    lib.grouped_dgrad(Dd, Wd, ed, dX)
+    assert torch.equal(dX.cpu(), R.grouped(dY, W, ends, False)[0].to(BF))
+    dW = torch.full((E, N, K), float("nan"), device="cuda")
+    lib.grouped_wgrad(Xd, Dd, ed, dW)
+    assert torch.equal(dW.cpu(), R.grouped_wgrad(X, dY, ends).float())
+    # fp8 codes of the same integers, scales that are powers of two
+    xs = torch.pow(2.0, torch.randint(-3, 4, (T,), generator=gen(4)).float())
+    ws = torch.pow(2.0, torch.randint(-3, 4, (E, N), generator=gen(5)).float())
+    lib.grouped_gemm(Xd.to(FP8), Wd.to(FP8), ed, Y.fill_(float("nan")), x_scale=xs.cuda(), w_scale=ws.cuda())
+    want = R.grouped(X.to(R.F64) * xs.to(R.F64)[:, None], W.to(R.F64) * ws.to(R.F64)[..., None], ends, True)[0]
+    assert torch.equal(Y.cpu(), want.to(BF))
+
+
+@pytest.mark.parametrize("T,E,N,K", [(700, 3, 512, 1408), (64, 64, 256, 2048)])
+def test_grouped_products_real_values(lib, T, E, N, K):
+    g = gen(T)
+    X, dY, W = torch.randn(T, K, generator=g).to(BF), torch.randn(T, N, generator=g).to(BF), torch.randn(E, N, K, generator=g).to(BF)
+    ends = torch.randint(0, T + 1, (E,), generator=g).sort().values.to(torch.int32)
+    ends[-1] = T
+    Y, dX = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, K, dtype=BF, device="cuda")
+    lib.grouped_gemm(X.cuda(), W.cuda(), ends.cuda(), Y)
+    want, mag = R.grouped(X, W, ends, True)
+    near(Y, want, K * R.U * mag + HALF[BF] * want.abs() + 2.0 ** -133)
+    lib.grouped_dgrad(dY.cuda(), W.cuda(), ends.cuda(), dX)
+    want, mag = R.grouped(dY, W, ends, False)
+    near(dX, want, N * R.U * mag + HALF[BF] * want.abs() + 2.0 ** -133)
+    dW = torch.empty(E, N, K, device="cuda")
+    lib.grouped_wgrad(X.cuda(), dY.cuda(), ends.cuda(), dW)
+    near(dW, R.grouped_wgrad(X, dY, ends), T * R.U * R.grouped_wgrad(X.abs(), dY.abs(), ends) + 2.0 ** -140)
+
+
+def test_grouped_rows_stay_apart(lib):
+    """NaN and infinities in one group's rows, and in rows of no group, reach no other group."""
+    ends, T, N, K = [70, 140, 210], 250, 256, 384
+    X, dY, W = ints((T, K), 3, 1), ints((T, N), 3, 2), ints((3, N, K), 3, 3)
+    X[70:140], dY[70:140], X[210:], dY[210:] = float("nan"), float("inf"), float("nan"), float("inf")
+    ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    clean = X.nan_to_num(0), dY.nan_to_num(0, 0, 0)
+    Y, dX = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, K, dtype=BF, device="cuda")
+    dW = torch.empty(3, N, K, device="cuda")
+    lib.grouped_gemm(X.cuda(), W.cuda(), ed, Y)
+    lib.grouped_dgrad(dY.cuda(), W.cuda(), ed, dX)
+    lib.grouped_wgrad(X.cuda(), dY.cuda(), ed, dW)
+    rows = torch.cat([torch.arange(70), torch.arange(140, 250)])
+    assert torch.equal(Y.cpu()[rows], R.grouped(clean[0], W, ends, True)[0].to(BF)[rows])
+    assert torch.equal(dX.cpu()[rows], R.grouped(clean[1], W, ends, False)[0].to(BF)[rows])
+    assert torch.equal(dW.cpu()[[0, 2]], R.grouped_wgrad(*clean, ends).float()[[0, 2]])
+    assert torch.isnan(Y[70:140]).all() and torch.isnan(dW[1]).all()
+
+
+def test_grouped_ends_out_of_order_are_clamped(lib):
+    """Ends outside [0, T] or falling are taken as the header says."""
+    ends, T, N, K = [-5, 60, 40, 10 ** 6, 100], 130, 128, 128
+    X, dY, W = ints((T, K), 3, 1), ints((T, N), 3, 2), ints((5, N, K), 3, 3)
+    ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    Y, dW = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(5, N, K, device="cuda")
+    lib.grouped_gemm(X.cuda(), W.cuda(), ed, Y)
+    lib.grouped_wgrad(X.cuda(), dY.cuda(), ed, dW)
+    assert torch.equal(Y.cpu(), R.grouped(X, W, ends, True)[0].to(BF))
+    assert torch.equal(dW.cpu(), R.grouped_wgrad(X, dY, ends).float())
+
+
+def test_grouped_offsets_past_32_bits(lib):
+    """An output of more than 2^31 elements (4.6 GiB)."""
+    T, N, K = 150_000, 16384, 128
+    X, W = ints((T, K), 3, 1), ints((2, N, K), 3, 2)
+    ends = [75_001, T]
+    Y = torch.empty(T, N, dtype=BF, device="cuda")
+    lib.grouped_gemm(X.cuda(), W.cuda(), torch.tensor(ends, dtype=torch.int32, device="cuda"), Y)
+    for a, b, e in ((0, 64, 0), (74_950, 75_001, 0), (75_001, 75_050, 1), (T - 70, T, 1)):
+        assert torch.equal(Y[a:b].cpu(), (X[a:b].to(R.F64) @ W[e].to(R.F64).t()).to(BF))
+
+
+# ------------------------------------------------------------------ the step of every expert
+def states(fmt, n, seed):
+    """Moments of n elements as (tensor, scale) pairs on the GPU."""
+    g = gen(seed)
+    m, v = 1e-3 * torch.randn(n, generator=g), (1e-2 * torch.randn(n, generator=g)) ** 2
+    if fmt == "f32":
+        return (m.cuda(), None), (v.cuda(), None)
+    nb = -(-n // 64)
+    return ((torch.randint(-127, 128, (n,), generator=g).to(torch.int8).cuda(), (1e-3 * torch.rand(nb, generator=g)).cuda()),
+            (torch.randint(0, 256, (n,), generator=g).to(torch.uint8).cuda(), (1e-4 * torch.rand(nb, generator=g)).cuda()))
+
+
+HYPER = {"lr": 1e-2, "beta1": 0.9, "beta2": 0.99, "eps": 1e-8, "weight_decay": 0.1, "momentum": 0.9, "alpha": 0.95}
+RULES = {"adamw": "mv", "nadam": "mv", "radam": "mv", "lion": "m", "rmsprop": "v", "adagrad": "v", "sgd": "", "sgd_momentum": "m"}
+
+
+def pick(opt, m, v):
+    return (m if "m" in RULES[opt] else (None, None)), (v if "v" in RULES[opt] else (None, None))
+
+
+@pytest.mark.parametrize("opt", RULES)
+@pytest.mark.parametrize("fmt", ["f32", "linear", "dynamic"])
+def test_grouped_step_equals_gradient_then_step(lib, opt, fmt):
+    """Bitwise the grouped gradient followed by the unfused step of the stacked weight."""
+    smap = "dynamic" if fmt == "dynamic" else "linear"
+    for N, K, ends, T in ((384, 256, [0, 33, 200, 200, 511], 515), (256, 128, [31], 31)):
+        E = len(ends)
+        g = gen(N)
+        X, dY = torch.randn(T, K, generator=g).to(BF).cuda(), (0.1 * torch.randn(T, N, generator=g)).to(BF).cuda()
+        ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+        W0 = (0.05 * torch.randn(E, N, K, generator=g)).to(BF).cuda()
+        (m, ms), (v, vs) = pick(opt, *states(fmt, E * N * K, 7))
+        for sr in (True, False):
+            a, b = ([None if t is None else t.clone() for t in (W0, m, v, ms, vs)] for _ in range(2))
+            sh = lambda t: None if t is None else t.view(E, N, K)  # noqa: E731
+            kw = dict(opt=opt, hyper=HYPER, step=3, seed=11, sr=sr, state_map=smap)
+            lib.grouped_wgrad_step(X, dY, ed, a[0], sh(a[1]), sh(a[2]), m_scale=a[3], v_scale=a[4], **kw)
+            dW = torch.empty(E, N, K, device="cuda")
+            lib.grouped_wgrad(X, dY, ed, dW)
+            flat = lambda t: None if t is None else t.view(E * N, K)  # noqa: E731
+            lib.optimizer_step(flat(dW), flat(b[0]), flat(b[1]), flat(b[2]), m_scale=b[3], v_scale=b[4], **kw)
+            for x, y, name in zip(a, b, ("W", "m", "v", "m scales", "v scales")):
+                assert x is None or torch.equal(x.view(-1), y.view(-1)), (name, sr)
+
+
+def test_grouped_step_against_the_definition(lib):
+    N, K, T, ends = 256, 384, 300, [100, 100, 300]
+    g = gen(5)
+    X, dY = torch.randn(T, K, generator=g).to(BF), (0.1 * torch.randn(T, N, generator=g)).to(BF)
+    W = (0.05 * torch.randn(3, N, K, generator=g)).to(BF)
+    (m, _), (v, _) = states("f32", 3 * N * K, 8)
+    m, v = m.view(3, N, K), v.view(3, N, K)
+    grad = R.grouped_wgrad(X, dY, ends)
+    gtol = T * R.U * R.grouped_wgrad(X.abs(), dY.abs(), ends)
+    w1, m1, v1 = R.adamw(W, grad, m.cpu(), v.cpu(), HYPER, 4)
+    Wd = W.cuda()
+    lib.grouped_wgrad_step(X.cuda(), dY.cuda(), torch.tensor(ends, dtype=torch.int32, device="cuda"), Wd, m, v, opt="adamw",
+                           hyper=HYPER, step=4, seed=1, sr=False)
+    near(m, m1, 0.1 * gtol + 4 * R.U * (m1.abs() + 0.1 * grad.abs()) + 2.0 ** -140)
+    near(v, v1, 0.01 * gtol * (2 * grad.abs() + gtol) + 6 * R.U * v1 + 2.0 ** -140)
+    # the update changes with the gradient's error by at most lr / (bias corrections) (|dm| + |m| |dv| / 2 v) / sqrt(v),
+    # and is computed in a dozen fp32 operations (two of them approximate to one step)
+    root = (v1 / (1 - 0.99 ** 4)).sqrt()
+    upd = 1e-2 / (1 - 0.9 ** 4) / root
+    dv = 0.01 * gtol * (2 * grad.abs() + gtol)
+    tol = upd * (0.1 * gtol + m1.abs() * dv / v1) + 24 * R.U * (upd * (m1.abs() + 0.1 * grad.abs()) + w1.abs())
+    near(Wd, w1, tol + HALF[BF] * (w1.abs() + tol))
+
+
+# ------------------------------------------------------------------ the step over many tensors
+SIZES = [1, 3, 4, 63, 64, 65, 127, 0, 1000, 4095, 4096, 4097, 4100, 5119, 8192 + 64, 70_001]
+
+
+@pytest.mark.parametrize("opt", RULES)
+@pytest.mark.parametrize("fmt", ["f32", "linear", "dynamic"])
+def test_multi_step_equals_the_unfused_step(lib, opt, fmt):
+    """Every tensor, with every type and rounding, bitwise as forge_optimizer_step of the same tensor
+    padded with zeros to its 128 x 128 blocks; nothing past its end is touched."""
+    smap = "dynamic" if fmt == "dynamic" else "linear"
+    hypers = [HYPER, dict(HYPER, lr=3e-3, weight_decay=0.0)]
+    for wt in (F32, BF):
+        for gt, sr in ((F32, True), (BF, False)):
+            W, G, M, V, MS, VS, whole = [], [], [], [], [], [], []
+            for i, n in enumerate(SIZES):
+                pad = (n // 16384 + 1) * 16384
+                g = gen(i)
+                keep = (torch.arange(pad) < n)
+                w = (0.05 * torch.randn(pad, generator=g) * keep).to(wt).cuda()
+                gr = (0.1 * torch.randn(pad, generator=g) * keep).to(gt).cuda()
+                (m, ms), (v, vs) = pick(opt, *states(fmt, pad, i + 50))
+                for t in (m, v):
+                    if t is not None:
+                        t.mul_(keep.cuda().to(t.dtype))
+                whole.append((w, gr, m, v, ms, vs))
+                nb = -(-n // 64)
+                for lst, t, k in ((W, w, n), (G, gr, n), (M, m, n), (V, v, n), (MS, ms, nb), (VS, vs, nb)):
+                    lst.append(None if t is None else t[:k])
+            want = [[None if t is None else t.clone() for t in s] for s in whole]
+            some = lambda lst: None if lst[0] is None else lst  # noqa: E731
+            plan = lib.MultiStep(W, G, some(M), some(V), m_scale=some(MS), v_scale=some(VS),
+                                 group=[i % 2 for i in range(len(SIZES))], opt=opt, state_map=smap)
+            for step in (1, 2):
+                plan.step(step=step, hyper=hypers, sr=sr)
+                for i, (w, gr, m, v, ms, vs) in enumerate(want):
+                    sq = lambda t: None if t is None else t.view(-1, 128)  # noqa: E731
+                    lib.optimizer_step(sq(gr.float()), sq(w), sq(m), sq(v), opt=opt, hyper=hypers[i % 2], step=step,
+                                       seed=i, m_scale=ms, v_scale=vs, sr=sr, state_map=smap)
+            for i, (got, exp) in enumerate(zip(whole, want)):
+                n = SIZES[i]
+                for k, (x, y) in enumerate(zip(got, exp)):
+                    if x is None or k == 1:
+                        continue
+                    c = -(-n // 64) if k >= 4 else n
+                    assert torch.equal(x[:c], y[:c]), (n, k)
+                for k, before in ((0, 0.0), (2, 0), (3, 0)):
+                    if got[k] is not None:
+                        assert bool((got[k][n:] == before).all()), (n, k)
+
+
+def test_multi_step_against_the_definition(lib):
+    n = 5003
+    g = gen(1)
+    w, gr = 0.05 * torch.randn(n, generator=g), 0.1 * torch.randn(n, generator=g)
+    (m, _), (v, _) = states("f32", n, 3)
+    gs = torch.tensor([0.25], device="cuda")
+    w1, m1, v1 = R.adamw(w, gr.to(R.F64) * 0.25, m.cpu(), v.cpu(), HYPER, 7)
+    wd = w.cuda()
+    plan = lib.MultiStep([wd], [gr.cuda()], [m], [v], opt="adamw")
+    plan.step(step=7, hyper=HYPER, grad_scale=gs)
+    near(m, m1, 4 * R.U * (m1.abs() + 0.1 * gr.abs()) + 2.0 ** -140)
+    near(v, v1, 6 * R.U * v1 + 2.0 ** -140)
+    upd = (1e-2 / (1 - 0.9 ** 7)) * (m1.abs() + 0.1 * gr.to(R.F64).abs()) / (v1 / (1 - 0.99 ** 7)).sqrt()
+    near(wd, w1, 24 * R.U * (upd + w1.abs()))
+
+
+def test_multi_step_8bit_against_the_definition(lib):
+    """Codes and scales of a tensor whose last block is short, from the definition of the linear map."""
+    n = 64 * 9 + 21
+    (m, ms), (v, vs) = states("linear", n, 4)
+    g = gen(2)
+    w, gr = 0.05 * torch.randn(n, generator=g), 0.1 * torch.randn(n, generator=g)
+    rep = lambda s: s.cpu().to(R.F64).repeat_interleave(64)[:n]  # noqa: E731
+    w1, m1, v1 = R.adamw(w, gr, m.cpu().to(R.F64) * rep(ms) / 127, v.cpu().to(R.F64) * rep(vs) / 255, HYPER, 2)
+    wd = w.cuda()
+    plan = lib.MultiStep([wd], [gr.cuda()], [m], [v], m_scale=[ms], v_scale=[vs], opt="adamw")
+    plan.step(step=2, hyper=HYPER)
+    for code, scale, exact, levels in ((m, ms, m1, 127), (v, vs, v1, 255)):
+        top = torch.stack([b.abs().max() for b in exact.split(64)])
+        near(scale, top, 8 * R.U * (top + 0.1))
+        got = code.cpu().to(R.F64) * rep(scale) / levels
+        # half a code of the block's map, a whole one where a positive v takes code 1 in place of 0
+        half = rep(scale) / levels * torch.where((exact > 0) & (code.cpu() == 1) & (levels == 255), 1.0, 0.5)
+        near(got, exact, half + 8 * R.U * (exact.abs() + 0.1))
+
+
+def test_multi_step_past_2_31_elements(lib):
+    n = 2 ** 31 + 4096 + 5
+    w, g = torch.zeros(n, dtype=BF, device="cuda"), torch.zeros(n, dtype=BF, device="cuda")
+    at = torch.tensor([0, 5000, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 4095, n - 6, n - 5, n - 1], device="cuda")
+    g[at] = -1.0
+    lib.MultiStep([w], [g], opt="sgd").step(step=1, hyper={"lr": 0.5}, sr=False)
+    assert bool((w[at] == 0.5).all()) and int((w != 0).sum()) == at.unique().numel()
+
+
+def test_multi_step_grads_and_stream(lib):
+    """set_grads takes other tensors; a step on another stream than the tensors'."""
+    w = [torch.zeros(300, device="cuda"), torch.zeros(5000, device="cuda")]
+    plan = lib.MultiStep(w, [torch.ones_like(t) for t in w], opt="sgd")
+    plan.step(step=1, hyper={"lr": 1.0})
+    plan.set_grads([torch.full_like(t, 2.0) for t in w])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        plan.step(step=2, hyper={"lr": 1.0})
+    s.synchronize()
+    assert all(bool((t == -3.0).all()) for t in w)
+
+
+def test_layer_step_in_a_graph(lib):
+    """Norm, products and steps captured once and replayed: every replay equals the eager pass."""
+    T, D, N, E = 200, 256, 384, 3
+    g = gen(4)
+    x, r, gain = torch.randn(T, D, generator=g).to(BF).cuda(), torch.randn(T, D, generator=g).to(BF).cuda(), torch.ones(D, device="cuda")
+    W0 = (0.05 * torch.randn(E, N, D, generator=g)).to(BF).cuda()
+    ends = torch.tensor([20, 20, 190], dtype=torch.int32, device="cuda")
+    dY = (0.1 * torch.randn(T, N, generator=g)).to(BF).cuda()
+
+    def buffers():
+        z = lambda *s, dtype=F32: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+        return dict(W=W0.clone(), m=z(E, N, D), v=z(E, N, D), gain=gain.clone(), gm=z(D), gv=z(D), dgain=z(D), h=z(T, D, dtype=BF),
+                    y=z(T, D, dtype=BF), rstd=z(T), Y=z(T, N, dtype=BF), dx=z(T, D, dtype=BF), dh=z(T, D, dtype=BF),
+                    ws=lib.rmsnorm_backward_workspace(T, D))
+
+    def run(b, plan):
+        lib.rmsnorm(x, b["gain"], b["y"], residual=r, h=b["h"], rstd=b["rstd"])
+        lib.grouped_gemm(b["y"], b["W"], ends, b["Y"])
+        lib.grouped_dgrad(dY, b["W"], ends, b["dx"])
+        lib.grouped_wgrad_step(b["y"], dY, ends, b["W"], b["m"], b["v"], opt="adamw", hyper=HYPER, step=5, seed=1)
+        lib.rmsnorm_backward(b["dx"], b["h"], b["gain"], b["rstd"], b["dh"], b["dgain"], workspace=b["ws"])
+        plan.step(step=5, hyper=HYPER)
+
+    a, c = buffers(), buffers()
+    pa, pc = (lib.MultiStep([b["gain"]], [b["dgain"]], [b["gm"]], [b["gv"]], opt="adamw") for b in (a, c))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run(c, pc)
+    for _ in range(3):
+        run(a, pa)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in a:
+            assert k == "ws" or torch.equal(a[k], c[k]), k
