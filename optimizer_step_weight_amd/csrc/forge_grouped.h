@@ -16,11 +16,11 @@ namespace forge {
 namespace grp {
 
 using ml2::barrier;
-using ml2::dma16;
 using ml2::floatx4;
 using ml2::make_rsrc;
 using ml2::wait_vm;
 typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
 
 // Position of workgroup b in an order of `total` tiles in which each XCD (b mod 8) has a
@@ -130,251 +130,413 @@ __device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T,
   return false;
 }
 
-// ------------------------------------------------------------------ row products
-// A BM x 256 tile of the output by one workgroup of 8 waves (2 of rows x 4 of 64 columns), the
-// contraction in slabs of 64 bytes (32 bf16 or 64 fp8 elements) held in 4 stages of LDS, three
-// in flight by LDS DMA while one is multiplied (the data path of forge_mainloop2.h):
-//  * A: BM rows of 64 bytes, read as 16-byte pieces (dY of the dgrad tiles); rows past the
-//    tile's last and contractions past the operand read as zero (buffer range check);
-//  * NT: W's rows n0 .. n0 + 255 the same way.  With both operands contraction-contiguous a
-//    lane's 8 (fp8: 32) contraction elements are consecutive;
-//  * NN: 32 rows of W of 512 bytes (256 columns), read by LDS transpose reads.
-// 16-byte chunks of the 64-byte rows are XOR-swizzled with (row / 4) mod 4: a group of 16 lanes
-// reads 16 rows in 16 distinct bank windows.
-template <int BM_, int MODE_>
-struct RowsPipe {
-  static constexpr int BM = BM_, MODE = MODE_, BN = 256, STAGES = 4, ROW = 64;
-  static constexpr int MB = BM / 32;                      // 16-row blocks of a wave
-  static constexpr int PANEL_A = BM * ROW, PANEL_B = 16384;
-  static constexpr int STAGE = PANEL_A + PANEL_B, SMEM = STAGES * STAGE;
-  static constexpr int DMA_A = BM >= 128 ? BM / 128 : 1, DMA = DMA_A + 2;  // 1 KiB copies per wave per slab
-  static constexpr int ESZ = MODE == FORGE_GROUPED_NT8 ? 1 : 2;
-  static_assert(BM == 64 || BM == 128 || BM == 256, "tile height");
+// ------------------------------------------------------------------ the contraction
+// D[second, first] = sum over c of second[c] first[c]: a tile of 64 MB rows ("second") by 64 NB
+// columns ("first", contiguous in the output) by one workgroup of 4 waves (2 x 2), a wave 32 MB x
+// 32 NB of it in 32 x 32 matrix blocks.  256 x 256 tiles read the least of L2 and LDS for their
+// products: a wave multiplies 16 blocks for 8 fragments.
+//
+// The contraction goes in slabs of 128 bytes of a row (64 bf16 or 128 fp8 elements), copied to LDS
+// by DMA in whole 128-byte lines: L2 answers a request a line, and with half lines (slabs of 64
+// bytes) its request rate, not its bytes, held the matrix cores at 62 % busy.  LDS holds three slabs of the
+// second operand and two of the first (160 KiB for 256 x 256).  A wave holds the fragments of two
+// half slabs in registers: while it multiplies one it reads the next from LDS.  step() has the
+// timetable.
+//
+// An operand lies in memory either
+//  * contraction-contiguous (TR = false: X, dY, W of the forward product): rows of 128 bytes in
+//    LDS, a fragment (lane l: row l mod 32, 8 bf16 from 8 (l / 32) or 32 fp8 from 32 (l / 32))
+//    read in 16-byte pieces.  The eight 16-byte chunks of a row are XOR-swizzled with
+//    (row / 2) mod 8: 16 consecutive rows at one chunk fall in 16 distinct bank windows; or
+//  * contraction-strided (TR = true: W of dgrad, X and dY of wgrad): 64 rows of the tile's width,
+//    read by LDS transpose reads: lane i of 16 points at row base + i / 4, columns 4 (i mod 4)
+//    .. + 3 and receives rows base .. base + 3 of column i.  Chunks are XOR-swizzled with
+//    4 (row mod 4): the four rows that 32 lanes read fall in four distinct 64-byte windows.
+// Reads past an operand's last row give zero (buffer range check).
+constexpr int THREADS = 256;
+
+template <int E_, bool TR_, int WIDTH_>  // element bytes, layout, rows (or columns) of the tile
+struct Side {
+  static constexpr int ESZ = E_, WIDTH = WIDTH_;
+  static constexpr bool TR = TR_;
+  static constexpr int PANEL = WIDTH * 128;                // bytes a slab
+  static constexpr int ROW = TR ? WIDTH * 2 : 128;         // bytes of a row in LDS
+  static constexpr int CPR = ROW / 16, RPD = 64 / CPR;     // chunks of a row, rows of a 1 KiB copy
+  static constexpr int DMA = PANEL / 4096;                 // copies of a wave a slab
+  static constexpr int M = ESZ == 2 ? 16 : 32;             // side of a matrix block
+  static constexpr int BLOCKS = WIDTH / 2 / M;             // blocks of a wave
+  static_assert(!TR || (ESZ == 2 && WIDTH >= 128), "transpose reads are of 16-bit elements");
+  static __device__ __forceinline__ int swz(int r) { return TR ? 4 * (r & 3) + 2 * ((r >> 3) & 1) : (r >> 1) & 7; }
 };
 
-struct RowsFeed {
-  u32x4 rA, rB;
-  uint32_t offA[2], offB[2];
-  uint32_t stepB;
+// One copy of 1 KiB: 16 bytes a lane from rsrc + off to LDS address `lds` + AT + 16 lane.  Two
+// instructions, because a wave issues one in 4 cycles: three fit beside a 16 x 16 x 32 product, and
+// more would keep the matrix core waiting.  Completion is awaited with wait_vm.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int AT>
+__device__ __forceinline__ void copy_1k(const u32x4& rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_add_u32 m0, %0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(lds), "i"(AT), "v"(off), "s"(rsrc)
+               : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+
+// Copies of an operand, slab after slab.
+template <class S>
+struct Feed {
+  u32x4 rsrc;               // from the next slab to be copied to the operand's end
+  uint32_t step;            // bytes from slab to slab
+  int slabs;                // left from there
+  uint32_t off[S::DMA];     // of this lane's pieces
+
+  // first: the tile's first element; bytes: from there to the operand's end; ld: row length in bytes.
+  __device__ __forceinline__ void open(const void* first, uint32_t bytes, uint32_t ld, int slabs_) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    rsrc = make_rsrc(first, bytes);
+    step = S::TR ? 64u * ld : 128u;
+    slabs = slabs_;
+#pragma unroll
+    for (int j = 0; j < S::DMA; ++j) {
+      const int r = S::RPD * (S::DMA * wave + j) + lane / S::CPR;
+      off[j] = (uint32_t)r * ld + 16u * (uint32_t)((lane % S::CPR) ^ S::swz(r));
+    }
+  }
+  // To the next slab, in two parts.  Past the last one the buffer is empty: its copies touch no
+  // memory, so that the loop has one body for all slabs.
+  __device__ __forceinline__ void next_base() {
+    const uint64_t b = ((uint64_t)rsrc.y << 32 | rsrc.x) + step;
+    rsrc.x = (uint32_t)b;
+    rsrc.y = (uint32_t)(b >> 32);
+    asm volatile("" : "+s"(rsrc));
+  }
+  __device__ __forceinline__ void next_bytes() {
+    const uint32_t left = rsrc.z - step;
+    --slabs;
+    rsrc.z = slabs > 0 ? left : 0u;
+    asm volatile("" : "+s"(rsrc));
+  }
+  __device__ __forceinline__ void next() {
+    next_base();
+    next_bytes();
+  }
 };
 
-__device__ __forceinline__ int swz_d(int row) { return (row >> 2) & 3; }
+typedef short v8i16 __attribute__((ext_vector_type(8)));
 
-template <class P>
-__device__ __forceinline__ void make_feed(RowsFeed& f, const GroupedArgs& a, const RowTile& t) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t C = P::MODE == FORGE_GROUPED_NN ? a.N : a.K;  // contraction length
-  const int64_t crow = C * P::ESZ;
-  f.rA = make_rsrc(static_cast<const unsigned char*>(a.A) + (int64_t)t.row0 * crow, (uint32_t)(t.rows * crow));
-#pragma unroll
-  for (int j = 0; j < P::DMA_A; ++j) {
-    // BM = 64 has 4 copies for 8 waves: waves 4-7 repeat those of waves 0-3 (the same bytes)
-    const int d = P::BM == 64 ? (wave & 3) : P::DMA_A * wave + j;
-    const int r = 16 * d + (lane >> 2), p = lane & 3;
-    f.offA[j] = (uint32_t)(r * crow + 16 * (p ^ swz_d(r)));
-  }
-  const unsigned char* W = static_cast<const unsigned char*>(a.W) + (int64_t)t.e * a.N * a.K * P::ESZ;
-  if constexpr (P::MODE == FORGE_GROUPED_NN) {
-    const int64_t k0 = (int64_t)t.n * P::BN;
-    f.rB = make_rsrc(W + k0 * 2, (uint32_t)(a.N * a.K * 2 - k0 * 2));
-    f.stepB = (uint32_t)(32 * a.K * 2);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = 2 * (2 * wave + j) + (lane >> 5), p = lane & 31;
-      f.offB[j] = (uint32_t)(r * a.K * 2 + 16 * (p ^ ml2::swz(r)));
-    }
-  } else {
-    const int64_t n0 = (int64_t)t.n * P::BN, left = a.N - n0;
-    f.rB = make_rsrc(W + n0 * crow, (uint32_t)((left < P::BN ? left : P::BN) * crow));
-    f.stepB = P::ROW;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = 16 * (2 * wave + j) + (lane >> 2), p = lane & 3;
-      f.offB[j] = (uint32_t)(r * crow + 16 * (p ^ swz_d(r)));
-    }
-  }
-}
-
-template <class P>
-__device__ __forceinline__ void issue(const RowsFeed& f, unsigned char* stage, int slab) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t sa = (uint32_t)slab * P::ROW, sb = (uint32_t)slab * f.stepB;
-#pragma unroll
-  for (int j = 0; j < P::DMA_A; ++j) {
-    const int d = P::BM == 64 ? (wave & 3) : P::DMA_A * wave + j;
-    dma16(f.rA, f.offA[j] + sa, stage + d * 1024);
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) dma16(f.rB, f.offB[j] + sb, stage + P::PANEL_A + (2 * wave + j) * 1024);
-}
-
-// 16 bytes at chunk c of row r of a 64-byte-row panel.
-__device__ __forceinline__ u32x4 piece(const unsigned char* panel, int r, int c) {
-  return *reinterpret_cast<const u32x4*>(panel + r * 64 + 16 * (c ^ swz_d(r)));
-}
-
-template <class P>
-struct Acc {
-  floatx4 v[P::MB][4];
+// A block over half a slab: bf16 16 rows x 32, fp8 32 rows x 64.
+template <int ESZ>
+struct Frag {
+  u32x4 q[ESZ == 2 ? 1 : 2];
 };
-template <int BM>
-struct Acc<RowsPipe<BM, FORGE_GROUPED_NT8>> {
-  floatx16 v[BM / 64][2];
-};
-
-// One slab: wave (wm, wn) multiplies rows wm BM / 2 .. and columns 64 wn ...
-template <class P>
-__device__ __forceinline__ void mma(Acc<P>& acc, const unsigned char* stage, int wm, int wn) {
-  const int lane = threadIdx.x & 63;
-  const unsigned char* pa = stage;
-  const unsigned char* pb = stage + P::PANEL_A;
-  if constexpr (P::MODE == FORGE_GROUPED_NT8) {
-    // 32 x 32 x 64: lane l holds the 32 codes 32 (l / 32) .. of row l mod 32
-    const int i = lane & 31, h = 2 * (lane >> 5);
-    auto frag8 = [&](const unsigned char* p, int row) {
-      const u32x4 lo = piece(p, row, h), hi = piece(p, row, h + 1);
-      intx8 x;
+// A wave's blocks in LDS: the addresses of this lane's pieces in a panel at address 0.  One piece is
+// read at v + the panel's place + a constant, so a half slab takes an addition for each v, not for
+// each piece.
+template <class S>
+struct View {
+  static constexpr int N = S::TR ? S::BLOCKS : (S::ESZ == 2 ? 2 : 4);
+  uint32_t v[N], at[2];
+  // first: the wave's first row (TR: column); less: taken off, as the places have it.
+  __device__ __forceinline__ void open(int first, int less) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (S::TR) {
+      const int i = lane & 15, r = 8 * (lane >> 4) + (i >> 2);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = (int)lo[j];
-        x[4 + j] = (int)hi[j];
-      }
-      return x;
-    };
-    intx8 b[2];
-#pragma unroll
-    for (int bj = 0; bj < 2; ++bj) b[bj] = frag8(pb, 64 * wn + 32 * bj + i);
-#pragma unroll
-    for (int bi = 0; bi < P::BM / 64; ++bi) {
-      const intx8 a = frag8(pa, wm * (P::BM / 2) + 32 * bi + i);
-#pragma unroll
-      for (int bj = 0; bj < 2; ++bj)
-        acc.v[bi][bj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b[bj], acc.v[bi][bj], 0, 0, 0, 127, 0, 127);
-    }
-  } else {
-    const int q = lane >> 4, i = lane & 15;
-    ml2::bf16x8 b[4];
-#pragma unroll
-    for (int bj = 0; bj < 4; ++bj) {
-      if constexpr (P::MODE == FORGE_GROUPED_NN)
-        b[bj] = ml2::frag(pb, 512, 4 * q + (i >> 2), 16 + 4 * q + (i >> 2), 64 * wn + 16 * bj, i);
-      else b[bj] = __builtin_bit_cast(ml2::bf16x8, piece(pb, 64 * wn + 16 * bj + i, q));
-    }
-#pragma unroll
-    for (int bi = 0; bi < P::MB; ++bi) {
-      const int row = wm * (P::BM / 2) + 16 * bi + i;
-      ml2::bf16x8 a;
-      if constexpr (P::MODE == FORGE_GROUPED_NN) a = ml2::dy_frag(pa, row, q);
-      else a = __builtin_bit_cast(ml2::bf16x8, piece(pa, row, q));
-#pragma unroll
-      for (int bj = 0; bj < 4; ++bj)
-        acc.v[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[bj], acc.v[bi][bj], 0, 0, 0);
-    }
-  }
-}
-
-// The whole contraction (none for rows of no group).  Ends with a barrier.
-template <class P>
-__device__ __forceinline__ void contract(Acc<P>& acc, unsigned char* smem, const GroupedArgs& a, const RowTile& t) {
-  const int wave = threadIdx.x >> 6, wm = wave >> 2, wn = wave & 3;
-  constexpr int NI = P::MODE == FORGE_GROUPED_NT8 ? P::BM / 64 : P::MB, NJ = P::MODE == FORGE_GROUPED_NT8 ? 2 : 4;
-  constexpr int NR = P::MODE == FORGE_GROUPED_NT8 ? 16 : 4;
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int r = 0; r < NR; ++r) acc.v[i][j][r] = 0.0f;
-  if (t.e >= a.E) return;  // nothing was staged: no barrier is needed
-  RowsFeed f;
-  make_feed<P>(f, a, t);
-  const int nsl = (int)((P::MODE == FORGE_GROUPED_NN ? a.N : a.K) * P::ESZ / P::ROW);
-#pragma unroll
-  for (int s = 0; s < P::STAGES - 1; ++s)
-    if (s < nsl) issue<P>(f, smem + s * P::STAGE, s);
-  for (int s = 0; s < nsl; ++s) {
-    const int ahead = min(nsl - 1 - s, P::STAGES - 2);
-    if (ahead >= 2) wait_vm<2 * P::DMA>();
-    else if (ahead == 1) wait_vm<P::DMA>();
-    else wait_vm<0>();
-    barrier();
-    if (s + P::STAGES - 1 < nsl) issue<P>(f, smem + ((s + P::STAGES - 1) % P::STAGES) * P::STAGE, s + P::STAGES - 1);
-    mma<P>(acc, smem + (s % P::STAGES) * P::STAGE, wm, wn);
-  }
-  barrier();
-}
-
-// Epilogue: the accumulators pass through LDS in fp32, 64 rows at a time (32 of either wave
-// row), and leave as bf16 (nearest even) in 16-byte stores; fp8 sums take their row's and
-// column's scales on the way.
-constexpr int OUT_LD = 256 + 4;                 // floats per staged row
-constexpr int OUT_BYTES = 64 * OUT_LD * 4;
-
-template <class P>
-__device__ __forceinline__ void store_tile(const Acc<P>& acc, unsigned char* smem, const GroupedArgs& a,
-                                           const RowTile& t) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3;
-  float* st = reinterpret_cast<float*>(smem);
-  const int64_t O = P::MODE == FORGE_GROUPED_NN ? a.K : a.N, o0 = (int64_t)t.n * P::BN;
-  uint16_t* out = static_cast<uint16_t*>(a.out);
-#pragma unroll
-  for (int part = 0; part < P::BM / 64; ++part) {
-    // staged row 32 wm + y is tile row wm BM / 2 + 32 part + y
-    if constexpr (P::MODE == FORGE_GROUPED_NT8) {
-      // 32 x 32 output: lane l, register r: row 8 (r / 4) + 4 (l / 32) + r mod 4, column l mod 32
-#pragma unroll
-      for (int bj = 0; bj < 2; ++bj)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          st[(32 * wm + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * OUT_LD + 64 * wn + 32 * bj + (lane & 31)] =
-              acc.v[part][bj][r];
+      for (int b = 0; b < N; ++b)
+        v[b] = (uint32_t)(r * S::ROW + 16 * ((first / 8 + 2 * b + ((i & 3) >> 1)) ^ S::swz(r)) + 8 * (i & 1) - less);
     } else {
+      const int r = first + (lane & (S::M - 1));  // `first` and M are multiples of 16: one swizzle for all blocks
 #pragma unroll
-      for (int b2 = 0; b2 < 2; ++b2)
-#pragma unroll
-        for (int bj = 0; bj < 4; ++bj)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            st[(32 * wm + 16 * b2 + 4 * (lane >> 4) + r) * OUT_LD + 64 * wn + 16 * bj + (lane & 15)] =
-                acc.v[2 * part + b2][bj][r];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {  // 64 rows x 32 pieces of 8 columns
-      const int id = tid + 512 * s, y = id >> 5, c = 8 * (id & 31);
-      const int row = (y >> 5) * (P::BM / 2) + 32 * part + (y & 31);
-      if (row >= t.rows || o0 + c >= O) continue;
-      const float* p = st + y * OUT_LD + c;
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[j];
-      if constexpr (P::MODE == FORGE_GROUPED_NT8) {
-        if (t.e < a.E) {
-          const float sa = a.a_scale[t.row0 + row];
-          const float* sw = a.w_scale + (int64_t)t.e * a.N + o0 + c;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= sa * sw[j];
-        }
+      for (int x = 0; x < N; ++x) {
+        const int c = S::ESZ == 2 ? 4 * x + (lane >> 4) : 4 * (x >> 1) + 2 * (lane >> 5) + (x & 1);
+        v[x] = (uint32_t)(r * 128 + 16 * (c ^ S::swz(r)) - less);
       }
-      u32x4 q;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = f32_to_bf16_rne(v[2 * j]) | (f32_to_bf16_rne(v[2 * j + 1]) << 16);
-      st16(out + (int64_t)(t.row0 + row) * O + o0 + c, q);
     }
-    __syncthreads();
+  }
+  // Piece KK of half H of block B.  Block 0 is read first.  (The empty asm keeps the compiler from
+  // folding the constants into v and adding the place for every piece.)
+  template <int B, int H, int KK>
+  __device__ __forceinline__ u32x4 read(uint32_t place) {
+    using P4 = __attribute__((address_space(3))) const u32x4*;
+    if constexpr (S::TR) {
+      using P2 = __attribute__((address_space(3))) ml2::v4i16*;
+      // rows r and r + 4 have the same swizzle
+      uint32_t at = v[B] + place;
+      asm("" : "+v"(at));
+      const ml2::v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P2)(at + 32 * H * S::ROW));
+      const ml2::v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P2)(at + (32 * H + 4) * S::ROW));
+      return __builtin_bit_cast(u32x4, (v8i16)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      if constexpr (B == 0) {
+        at[KK] = v[S::ESZ == 2 ? H : 2 * H + KK] + place;
+        asm("" : "+v"(at[KK]));
+      }
+      return *(P4)(at[KK] + B * S::M * 128);
+    }
+  }
+};
+
+template <class A, class B>  // second (rows), first (columns)
+struct Tile {
+  static constexpr int MB = A::BLOCKS, NB = B::BLOCKS, ESZ = A::ESZ, M = A::M;
+  static constexpr int PIECES = ESZ == 2 ? 1 : 2, READS = PIECES * (MB + NB);  // of half a slab
+  using Acc = std::conditional_t<ESZ == 2, floatx4, floatx16>;
+  static constexpr int STAGES_A = 3, STAGES_B = 2;
+  static constexpr int SMEM = STAGES_A * A::PANEL + STAGES_B * B::PANEL;
+  Acc acc[MB][NB];
+
+  struct Frags {
+    Frag<ESZ> a[MB], b[NB];
+  };
+
+  // d += b a.  A bf16 tile of 256 x 256 has 256 accumulators a lane, all the AGPRs that there are;
+  // the allocator then moves some to and fro within the loop.  The register kind is therefore
+  // named here: three quarters of them AGPRs, the rest VGPRs, with room left in both.  The compiler
+  // does not see that these are matrix instructions: settle() is due before anything else reads d.
+  template <int BLOCK>
+  static __device__ __forceinline__ void mma(Acc& d, const Frag<ESZ>& b, const Frag<ESZ>& a) {
+    if constexpr (ESZ == 2) {
+      if constexpr (BLOCK < 48) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(b.q[0]), "v"(a.q[0]));
+      else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(b.q[0]), "v"(a.q[0]));
+    } else {
+      auto whole = [](const Frag<1>& f) {
+        return intx8{(int)f.q[0][0], (int)f.q[0][1], (int)f.q[0][2], (int)f.q[0][3],
+                     (int)f.q[1][0], (int)f.q[1][1], (int)f.q[1][2], (int)f.q[1][3]};
+      };
+      d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(whole(b), whole(a), d, 0, 0, 0, 127, 0, 127);
+    }
+  }
+
+  // Waits until the last matrix instructions have written their accumulators.
+  static __device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  View<A> va;
+  View<B> vb;
+  // Read n of the fragments of half h of a slab at (pa, pb).
+  template <int H, int n>
+  __device__ __forceinline__ void read(Frags& f, uint32_t pa, uint32_t pb) {
+    constexpr int kk = n % PIECES, i = n / PIECES;
+    if constexpr (i < NB) f.b[i].q[kk] = vb.template read<i, H, kk>(pb);
+    else f.a[i - NB].q[kk] = va.template read<i - NB, H, kk>(pa);
+  }
+
+  // LDS addresses of the panels of slab s and slab s + 1 in either ring, and of the A panel that is
+  // being filled.  They include the wave's
+  // first copy, which the views' addresses take off again.
+  struct Places {
+    uint32_t a, a_next, a_fill, a_first, a_end, b, b_next, b_sum;
+    __device__ __forceinline__ void find_next() {
+      a_next = a + A::PANEL;
+      a_next = a_next == a_end ? a_first : a_next;
+      asm volatile("" : "+s"(a_next));
+      b_next = b_sum - b;
+      asm volatile("" : "+s"(b_next));
+    }
+  };
+
+  // How many of `many` things, spread evenly over the products [from, to), come before product n.
+  static constexpr int due(int many, int from, int to, int n) {
+    return n <= from ? 0 : n >= to ? many : (many * (n - from) + (to - from) - 1) / (to - from);
+  }
+
+  // Slab s, whose first half is in f, up to the first half of slab s + 1 in f.  In sixteenths of
+  // the H products of half a slab:
+  //    0 ..  7  the second half is read to g
+  //         10  it has been read by all waves (barrier): the place of slab s is free
+  //   10 .. 26  B of slab s + 2 is copied there, 26 .. 42 (10 of the next slab) A of slab s + 3
+  //         22  slab s + 1 has landed for all waves (barrier)
+  //   22 .. 29  its first half is read to f
+  // The copies keep one pace throughout, half of what the address unit takes: a faster one makes
+  // waves wait to issue them.  A copy has at least 1.75 H products' time to land, a read 3 / 16 H.
+  __device__ __forceinline__ void step(Frags& f, Frags& g, Feed<A>& fa, Feed<B>& fb, Places& at) {
+    constexpr int H = MB * NB;
+    constexpr int FREE = 10 * H / 16, LANDED = 22 * H / 16, G_END = 7 * H / 16, F_END = 29 * H / 16;
+    constexpr int A_FROM = 26 * H / 16;
+    static_for<2 * H>([&](auto nc) {
+      constexpr int n = decltype(nc)::value;
+      // the scalar work, a few instructions at a time
+      if constexpr (n == (G_END < FREE ? G_END : FREE)) fb.next_base();
+      if constexpr (n == (G_END + 1 < FREE ? G_END + 1 : FREE)) fb.next_bytes();
+      if constexpr (n == (FREE + 2 < A_FROM ? FREE + 2 : A_FROM)) fa.next_base();
+      if constexpr (n == (FREE + 3 < A_FROM ? FREE + 3 : A_FROM)) fa.next_bytes();
+      if constexpr (n == (FREE + 4 < LANDED ? FREE + 4 : LANDED)) at.find_next();
+      if constexpr (n == FREE) {
+        __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));
+        barrier();
+      }
+      if constexpr (n == LANDED) {
+        // copied later than slab s + 1: A of s + 2 and the first copies of B of s + 2
+        wait_vm<A::DMA + due(B::DMA, FREE, A_FROM, n)>();
+        barrier();
+      }
+      if constexpr (n == A_FROM) at.a_fill = at.a;
+      constexpr int b0 = due(B::DMA, FREE, A_FROM, n), b1 = due(B::DMA, FREE, A_FROM, n + 1);
+      static_for<b1 - b0>([&](auto k) {
+        constexpr int j = b0 + decltype(k)::value;
+        copy_1k<j * 1024>(fb.rsrc, fb.off[j], at.b);
+      });
+      constexpr int an = n < FREE ? n + 2 * H : n;
+      constexpr int a0 = due(A::DMA, A_FROM, FREE + 2 * H, an), a1 = due(A::DMA, A_FROM, FREE + 2 * H, an + 1);
+      static_for<a1 - a0>([&](auto k) {
+        constexpr int j = a0 + decltype(k)::value;
+        copy_1k<j * 1024>(fa.rsrc, fa.off[j], at.a_fill);
+      });
+      constexpr int g0 = due(READS, 0, G_END, n), g1 = due(READS, 0, G_END, n + 1);
+      static_for<g1 - g0>([&](auto k) { read<1, g0 + decltype(k)::value>(g, at.a, at.b); });
+      constexpr int f0 = due(READS, LANDED, F_END, n), f1 = due(READS, LANDED, F_END, n + 1);
+      static_for<f1 - f0>([&](auto k) { read<0, f0 + decltype(k)::value>(f, at.a_next, at.b_next); });
+      if constexpr (n < H) mma<n>(acc[n / NB][n % NB], f.b[n % NB], f.a[n / NB]);
+      else mma<n - H>(acc[n / NB - MB][n % NB], g.b[n % NB], g.a[n / NB - MB]);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    at.a = at.a_next;
+    at.b = at.b_next;
+  }
+  // Copies of A that a slab's end starts, before the next slab's beginning goes on.
+  static constexpr int A_EARLY = due(A::DMA, 26 * (MB * NB) / 16, 10 * (MB * NB) / 16 + 2 * MB * NB, 2 * MB * NB);
+
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < M * M / 64; ++r) acc[i][j][r] = 0.0f;
+  }
+
+  // The whole contraction over `slabs` slabs.  All waves call it; LDS must be free when it is
+  // called, and is free again after a further barrier.
+  __device__ __forceinline__ void contract(unsigned char* smem, Feed<A>& fa, Feed<B>& fb, int slabs) {
+    if (slabs == 0) return zero();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t to_a = lds_address(smem) + (uint32_t)(wave * A::DMA * 1024);
+    const uint32_t to_b = lds_address(smem) + STAGES_A * A::PANEL + (uint32_t)(wave * B::DMA * 1024);
+    static_for<3>([&](auto sc) {  // two slabs and the first copies of A of the third
+      constexpr int s = decltype(sc)::value;
+      if constexpr (s > 0) fa.next();
+      static_for<(s < 2 ? A::DMA : A_EARLY)>(
+          [&](auto j) { copy_1k<s * A::PANEL + j * 1024>(fa.rsrc, fa.off[j], to_a); });
+      if constexpr (s == 1) fb.next();
+      if constexpr (s < 2)
+        static_for<B::DMA>([&](auto j) { copy_1k<s * B::PANEL + j * 1024>(fb.rsrc, fb.off[j], to_b); });
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    zero();  // while the copies fly
+    va.open(M * MB * (wave >> 1), wave * A::DMA * 1024);
+    vb.open(M * NB * (wave & 1), wave * B::DMA * 1024);
+    wait_vm<A::DMA + B::DMA + A_EARLY>();
+    barrier();
+    Frags f, g;
+    static_for<READS>([&](auto n) { read<0, n>(f, to_a, to_b); });
+    Places at{to_a, 0, to_a + 2 * A::PANEL, to_a, to_a + STAGES_A * A::PANEL, to_b, 0, 2 * to_b + B::PANEL};
+    for (int s = slabs; s > 0; --s) step(f, g, fa, fb, at);
+    settle();
+    wait_vm<0>();  // no copy may land after the workgroup's end
+  }
+
+  // First row and column of block (i, j).  Of its M x M values lane l has row l mod M; element
+  // 4 g + r of the accumulator is column 4 (64 / M) g + 4 (l / M) + r.
+  static __device__ __forceinline__ int row_of(int i) { return M * (MB * (int)(threadIdx.x >> 7) + i); }
+  static __device__ __forceinline__ int col_of(int j) { return M * (NB * (int)((threadIdx.x >> 6) & 1) + j); }
+};
+
+// Two values to bf16, nearest even, in one instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+
+// ------------------------------------------------------------------ row products
+// Y_e = X_e W_e^T and dX_e = dY_e W_e.  A row tile is 256 rows, or the last rows of a group in the
+// least multiple of 64; the last columns of an odd multiple of 128 take a tile half as wide.
+template <int MODE, int HEIGHT, int WIDTH>  // of the tile, in 64s
+__device__ __forceinline__ void rows_tile(const GroupedArgs& a, const RowTile& t, unsigned char* smem) {
+  constexpr bool NN = MODE == FORGE_GROUPED_NN, FP8 = MODE == FORGE_GROUPED_NT8;
+  constexpr int ESZ = FP8 ? 1 : 2;
+  using A = Side<ESZ, false, 64 * HEIGHT>;
+  using B = Side<ESZ, NN, 64 * WIDTH>;
+  using T = Tile<A, B>;
+  const int64_t C = NN ? a.N : a.K, O = NN ? a.K : a.N, o0 = (int64_t)t.n * 256;
+  const int slabs = t.e < a.E ? (int)(C * ESZ / 128) : 0;  // rows of no group: zeros
+  Feed<A> fa;
+  Feed<B> fb;
+  fa.open(static_cast<const unsigned char*>(a.A) + (int64_t)t.row0 * C * ESZ, (uint32_t)(t.rows * C * ESZ),
+          (uint32_t)(C * ESZ), slabs);
+  const unsigned char* W = static_cast<const unsigned char*>(a.W) + (int64_t)t.e * a.N * a.K * ESZ;
+  if constexpr (NN) fb.open(W + o0 * 2, (uint32_t)(a.N * a.K * 2 - o0 * 2), (uint32_t)(a.K * 2), slabs);
+  else fb.open(W + o0 * C * ESZ, (uint32_t)(64 * WIDTH * C * ESZ), (uint32_t)(C * ESZ), slabs);
+  T tile;
+  tile.contract(smem, fa, fb, slabs);
+
+  const int lane = (int)threadIdx.x & 63;
+  uint16_t* out = static_cast<uint16_t*>(a.out);
+  const float* ws = FP8 && t.e < a.E ? a.w_scale + (int64_t)t.e * a.N + o0 : nullptr;
+#pragma unroll
+  for (int i = 0; i < T::MB; ++i) {
+    const int row = T::row_of(i) + (lane & (T::M - 1));
+    const bool in = row < t.rows;
+    uint16_t* p = out + (int64_t)(t.row0 + row) * O + o0;
+    if constexpr (FP8) {
+      const float sa = ws && in ? a.a_scale[t.row0 + row] : 1.0f;
+      const int hi = lane >> 5;
+#pragma unroll
+      for (int j = 0; j < T::NB; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          u32x2 q[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            floatx4u sw{1.0f, 1.0f, 1.0f, 1.0f};
+            if (ws) sw = *reinterpret_cast<const floatx4u*>(ws + T::col_of(j) + 8 * (g + h) + 4 * hi);
+            float v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = tile.acc[i][j][4 * (g + h) + r] * (sa * sw[r]);
+            q[h] = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+          }
+          // the lower half wave's columns 8 (g + 1) .. + 3 against the upper half's 8 g + 4 .. + 7: a
+          // lane then has 8 consecutive columns, from 8 g in the lower and 8 (g + 1) in the upper half
+          const auto x = __builtin_amdgcn_permlane32_swap(q[0].x, q[1].x, false, false);
+          const auto y = __builtin_amdgcn_permlane32_swap(q[0].y, q[1].y, false, false);
+          if (in) st16(p + T::col_of(j) + 8 * (g + hi), u32x4{x[0], y[0], x[1], y[1]});
+        }
+    } else {
+      const int q = lane >> 4;
+#pragma unroll
+      for (int j = 0; j < T::NB; j += 2) {
+        const floatx4 u = tile.acc[i][j], v = tile.acc[i][j + 1];
+        // odd 16-lane rows of block j against even ones of block j + 1: a lane then has 8 consecutive
+        // columns, of block j in even rows and of block j + 1 in odd ones
+        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(u[0], u[1]), pack_bf16(v[0], v[1]), false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(u[2], u[3]), pack_bf16(v[2], v[3]), false, false);
+        if (in) st16(p + T::col_of(j + (q & 1)) + 8 * (q >> 1), u32x4{x[0], y[0], x[1], y[1]});
+      }
+    }
   }
 }
 
-template <int BM, int MODE>
-__global__ __launch_bounds__(512, BM == 64 ? 4 : 2) void grouped_rows_kernel(GroupedArgs a) {
-  using P = RowsPipe<BM, MODE>;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[P::SMEM > OUT_BYTES ? P::SMEM : OUT_BYTES];
+template <int MODE>
+__global__ __launch_bounds__(THREADS, 1) void grouped_rows_kernel(GroupedArgs a) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * 32768];
   const int64_t O = MODE == FORGE_GROUPED_NN ? a.K : a.N;
   RowTile t;
-  if (!find_tile<BM>(a.ends, a.E, a.T, (int)((O + P::BN - 1) / P::BN), (int)blockIdx.x, t)) return;
-  Acc<P> acc;
-  contract<P>(acc, smem, a, t);
-  store_tile<P>(acc, smem, a, t);
+  if (!find_tile<256>(a.ends, a.E, a.T, (int)((O + 255) / 256), (int)blockIdx.x, t)) return;
+  const bool narrow = O - (int64_t)t.n * 256 < 256;
+  switch ((t.rows + 63) / 64 + (narrow ? 4 : 0)) {
+    case 1: rows_tile<MODE, 1, 4>(a, t, smem); break;
+    case 2: rows_tile<MODE, 2, 4>(a, t, smem); break;
+    case 3: rows_tile<MODE, 3, 4>(a, t, smem); break;
+    case 4: rows_tile<MODE, 4, 4>(a, t, smem); break;
+    case 5: rows_tile<MODE, 1, 2>(a, t, smem); break;
+    case 6: rows_tile<MODE, 2, 2>(a, t, smem); break;
+    case 7: rows_tile<MODE, 3, 2>(a, t, smem); break;
+    case 8: rows_tile<MODE, 4, 2>(a, t, smem); break;
+  }
 }
 
 }  // namespace grp

@@ -6,30 +6,18 @@
 
 namespace forge {
 
-namespace {
-
-template <int BM>
-int launch_rows(int mode, const GroupedArgs& a, hipStream_t st) {
+int launch_grouped_rows(int mode, const GroupedArgs& a, void* stream) {
   const int64_t O = mode == FORGE_GROUPED_NN ? a.K : a.N;
-  const int64_t tiles = (a.T / BM + (a.E < a.T ? a.E : a.T) + 1) * ((O + 255) / 256);
-  const dim3 grid((unsigned)tiles), block(512);
+  const int64_t tiles = (a.T / 256 + (a.E < a.T ? a.E : a.T) + 1) * ((O + 255) / 256);
+  const dim3 grid((unsigned)tiles), block(grp::THREADS);
+  hipStream_t st = (hipStream_t)stream;
   switch (mode) {
-    case FORGE_GROUPED_NT: hipLaunchKernelGGL((grp::grouped_rows_kernel<BM, FORGE_GROUPED_NT>), grid, block, 0, st, a); break;
-    case FORGE_GROUPED_NN: hipLaunchKernelGGL((grp::grouped_rows_kernel<BM, FORGE_GROUPED_NN>), grid, block, 0, st, a); break;
-    case FORGE_GROUPED_NT8: hipLaunchKernelGGL((grp::grouped_rows_kernel<BM, FORGE_GROUPED_NT8>), grid, block, 0, st, a); break;
+    case FORGE_GROUPED_NT: hipLaunchKernelGGL(grp::grouped_rows_kernel<FORGE_GROUPED_NT>, grid, block, 0, st, a); break;
+    case FORGE_GROUPED_NN: hipLaunchKernelGGL(grp::grouped_rows_kernel<FORGE_GROUPED_NN>, grid, block, 0, st, a); break;
+    case FORGE_GROUPED_NT8: hipLaunchKernelGGL(grp::grouped_rows_kernel<FORGE_GROUPED_NT8>, grid, block, 0, st, a); break;
     default: return (int)hipErrorInvalidValue;
   }
   return (int)hipGetLastError();
-}
-
-}  // namespace
-
-// The tile's height goes by the mean rows of a group, all that the host knows.
-int launch_grouped_rows(int mode, const GroupedArgs& a, void* stream) {
-  const int64_t mean = a.T / a.E;
-  if (mean >= 192) return launch_rows<256>(mode, a, (hipStream_t)stream);
-  if (mean >= 64) return launch_rows<128>(mode, a, (hipStream_t)stream);
-  return launch_rows<64>(mode, a, (hipStream_t)stream);
 }
 
 __global__ __launch_bounds__(ml2::THREADS, kOcc2) void grouped_wgrad_kernel(GroupedWgradArgs a, float* dW) {
