@@ -21,7 +21,6 @@ using ml2::make_rsrc;
 using ml2::wait_vm;
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef float floatx4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef int intx8 __attribute__((ext_vector_type(8)));
 
 // Position of workgroup b in an order of `total` tiles in which each XCD (b mod 8) has a
 // contiguous run.
@@ -151,22 +150,27 @@ __device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T,
 //  * contraction-strided (TR = true: W of dgrad, X and dY of wgrad): 64 rows of the tile's width,
 //    read by LDS transpose reads: lane i of 16 points at row base + i / 4, columns 4 (i mod 4)
 //    .. + 3 and receives rows base .. base + 3 of column i.  Chunks are XOR-swizzled with
-//    4 (row mod 4): the four rows that 32 lanes read fall in four distinct 64-byte windows.
+//    4 (row mod 4) + 2 (q mod 2): the eight half-windows that 32 lanes read are distinct.
 // Reads past an operand's last row give zero (buffer range check).
 constexpr int THREADS = 256;
 
-template <int E_, bool TR_, int WIDTH_>  // element bytes, layout, rows (or columns) of the tile
+// Element bytes, layout, rows (or columns) of the tile.  A lane's 8 contraction elements of a k-step of
+// 32 are 8 q .. 8 q + 7 (q = l / 16), or with FOURS 4 q .. + 3 and 16 + 4 q .. + 3: the order of the
+// fused step's contraction (forge_mainloop2.h), which gives its sums bit for bit.
+template <int E_, bool TR_, int WIDTH_, bool FOURS_ = false>
 struct Side {
   static constexpr int ESZ = E_, WIDTH = WIDTH_;
-  static constexpr bool TR = TR_;
+  static constexpr bool TR = TR_, FOURS = FOURS_;
+  static constexpr int R_LANE = FOURS ? 4 : 8, R_HIGH = FOURS ? 16 : 4;  // TR: rows from q to q + 1, to the second read
   static constexpr int PANEL = WIDTH * 128;                // bytes a slab
   static constexpr int ROW = TR ? WIDTH * 2 : 128;         // bytes of a row in LDS
   static constexpr int CPR = ROW / 16, RPD = 64 / CPR;     // chunks of a row, rows of a 1 KiB copy
   static constexpr int DMA = PANEL / 4096;                 // copies of a wave a slab
   static constexpr int M = ESZ == 2 ? 16 : 32;             // side of a matrix block
   static constexpr int BLOCKS = WIDTH / 2 / M;             // blocks of a wave
+  static_assert(TR || !FOURS, "only transpose reads take the rows in fours");
   static_assert(!TR || (ESZ == 2 && WIDTH >= 128), "transpose reads are of 16-bit elements");
-  static __device__ __forceinline__ int swz(int r) { return TR ? 4 * (r & 3) + 2 * ((r >> 3) & 1) : (r >> 1) & 7; }
+  static __device__ __forceinline__ int swz(int r) { return TR ? 4 * (r & 3) + 2 * ((r / R_LANE) & 1) : (r >> 1) & 7; }
 };
 
 // One copy of 1 KiB: 16 bytes a lane from rsrc + off to LDS address `lds` + AT + 16 lane.  Two
@@ -242,7 +246,7 @@ struct View {
   __device__ __forceinline__ void open(int first, int less) {
     const int lane = threadIdx.x & 63;
     if constexpr (S::TR) {
-      const int i = lane & 15, r = 8 * (lane >> 4) + (i >> 2);
+      const int i = lane & 15, r = S::R_LANE * (lane >> 4) + (i >> 2);
 #pragma unroll
       for (int b = 0; b < N; ++b)
         v[b] = (uint32_t)(r * S::ROW + 16 * ((first / 8 + 2 * b + ((i & 3) >> 1)) ^ S::swz(r)) + 8 * (i & 1) - less);
@@ -262,11 +266,11 @@ struct View {
     using P4 = __attribute__((address_space(3))) const u32x4*;
     if constexpr (S::TR) {
       using P2 = __attribute__((address_space(3))) ml2::v4i16*;
-      // rows r and r + 4 have the same swizzle
+      // rows r and r + R_HIGH have the same swizzle
       uint32_t at = v[B] + place;
       asm("" : "+v"(at));
       const ml2::v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P2)(at + 32 * H * S::ROW));
-      const ml2::v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P2)(at + (32 * H + 4) * S::ROW));
+      const ml2::v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P2)(at + (32 * H + S::R_HIGH) * S::ROW));
       return __builtin_bit_cast(u32x4, (v8i16)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       if constexpr (B == 0) {
@@ -291,25 +295,25 @@ struct Tile {
     Frag<ESZ> a[MB], b[NB];
   };
 
-  // d += b a.  A bf16 tile of 256 x 256 has 256 accumulators a lane, all the AGPRs that there are;
-  // the allocator then moves some to and fro within the loop.  The register kind is therefore
-  // named here: three quarters of them AGPRs, the rest VGPRs, with room left in both.  The compiler
-  // does not see that these are matrix instructions: settle() is due before anything else reads d.
+  // d += b a.  A tile of 256 x 256 has 256 accumulators a lane, all the AGPRs that there are; the
+  // allocator then moves some to and fro within the loop.  The register kind is therefore named here:
+  // three quarters of them AGPRs, the rest VGPRs, with room left in both.  The compiler does not see
+  // that these are matrix instructions: settle() is due before anything else reads d.
   template <int BLOCK>
   static __device__ __forceinline__ void mma(Acc& d, const Frag<ESZ>& b, const Frag<ESZ>& a) {
+    constexpr bool AGPR = BLOCK * (M * M / 64) < 192;
     if constexpr (ESZ == 2) {
-      if constexpr (BLOCK < 48) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(b.q[0]), "v"(a.q[0]));
+      if constexpr (AGPR) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(b.q[0]), "v"(a.q[0]));
       else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(b.q[0]), "v"(a.q[0]));
     } else {
-      auto whole = [](const Frag<1>& f) {
-        return intx8{(int)f.q[0][0], (int)f.q[0][1], (int)f.q[0][2], (int)f.q[0][3],
-                     (int)f.q[1][0], (int)f.q[1][1], (int)f.q[1][2], (int)f.q[1][3]};
-      };
-      d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(whole(b), whole(a), d, 0, 0, 0, 127, 0, 127);
+      auto whole = [](const Frag<1>& f) { return __builtin_shufflevector(f.q[0], f.q[1], 0, 1, 2, 3, 4, 5, 6, 7); };
+      if constexpr (AGPR) asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %2, %0" : "+a"(d) : "v"(whole(b)), "v"(whole(a)));
+      else asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %2, %0" : "+v"(d) : "v"(whole(b)), "v"(whole(a)));
     }
   }
 
-  // Waits until the last matrix instructions have written their accumulators.
+  // Before and after the matrix instructions that the compiler does not see: every register written
+  // before is there (19 wait states at most, after a 32 x 32 x 64 product).
   static __device__ __forceinline__ void settle() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
@@ -435,16 +439,53 @@ struct Tile {
     Frags f, g;
     static_for<READS>([&](auto n) { read<0, n>(f, to_a, to_b); });
     Places at{to_a, 0, to_a + 2 * A::PANEL, to_a, to_a + STAGES_A * A::PANEL, to_b, 0, 2 * to_b + B::PANEL};
+    settle();  // the zeroes are written
     for (int s = slabs; s > 0; --s) step(f, g, fa, fb, at);
     settle();
     wait_vm<0>();  // no copy may land after the workgroup's end
   }
 
-  // First row and column of block (i, j).  Of its M x M values lane l has row l mod M; element
-  // 4 g + r of the accumulator is column 4 (64 / M) g + 4 (l / M) + r.
-  static __device__ __forceinline__ int row_of(int i) { return M * (MB * (int)(threadIdx.x >> 7) + i); }
-  static __device__ __forceinline__ int col_of(int j) { return M * (NB * (int)((threadIdx.x >> 6) & 1) + j); }
+  // First row and column of this wave in the tile.
+  static __device__ __forceinline__ int row0() { return M * MB * (int)(threadIdx.x >> 7); }
+  static __device__ __forceinline__ int col0() { return M * NB * (int)((threadIdx.x >> 6) & 1); }
+
+  // The tile to memory by rows.  A lane holds 4 consecutive columns of one of a block's M rows, and a
+  // store from there would touch 16 rows at once, 32 or 64 bytes of each.  So the M rows of a row of
+  // blocks pass through 8 KiB of the wave's own in LDS (no barrier: a wave's LDS accesses are in
+  // order), and leave as whole rows of the wave's M NB columns, 16 bytes a lane.  Chunks of 16 bytes
+  // are XOR-swizzled with the row.  pack(row, column, v): the 4 values of a row of the wave from that
+  // column on as they are stored (8 bytes bf16 or 16 fp32); put(row, column, q): stores 16 bytes.
+  template <class Unit, class Pack, class Put>
+  __device__ __forceinline__ void store(unsigned char* wave_lds, Pack&& pack, Put&& put) const {
+    constexpr int SIZE = sizeof(Unit) / 4;              // of an element
+    constexpr int ROW = M * NB * SIZE, CH = ROW / 16;   // bytes and chunks of a row
+    constexpr int MASK = (CH < 16 ? CH : 16) - 1;
+    const int lane = (int)threadIdx.x & 63, row = lane & (M - 1);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int g = 0; g < M * M / 256; ++g) {
+          const int c4 = M / 4 * j + 64 / M * g + lane / M;  // column / 4
+          const Unit u = pack(M * i + row, 4 * c4, floatx4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                                                           acc[i][j][4 * g + 3]});
+          const int byte = c4 * (int)sizeof(Unit);
+          *reinterpret_cast<Unit*>(wave_lds + row * ROW + 16 * ((byte >> 4) ^ (row & MASK)) + (byte & 15)) = u;
+        }
+      __builtin_amdgcn_wave_barrier();
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int t = 0; t < M * CH / 64; ++t) {
+        const int p = lane + 64 * t, r = p / CH, c = p % CH;
+        put(M * i + r, 16 / SIZE * c, *reinterpret_cast<const u32x4*>(wave_lds + r * ROW + 16 * (c ^ (r & MASK))));
+      }
+      __builtin_amdgcn_wave_barrier();
+      asm volatile("" ::: "memory");
+    }
+  }
 };
+constexpr int WAVE_LDS = 8192;
 
 // Two values to bf16, nearest even, in one instruction.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -474,50 +515,28 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, const RowTile& t
   T tile;
   tile.contract(smem, fa, fb, slabs);
 
-  const int lane = (int)threadIdx.x & 63;
-  uint16_t* out = static_cast<uint16_t*>(a.out);
-  const float* ws = FP8 && t.e < a.E ? a.w_scale + (int64_t)t.e * a.N + o0 : nullptr;
+  barrier();  // every wave is done with the slabs
+  const int row0 = T::row0(), col0 = T::col0();
+  uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(t.row0 + row0) * O + o0 + col0;
+  const float* ws = FP8 && t.e < a.E ? a.w_scale + (int64_t)t.e * a.N + o0 + col0 : nullptr;
+  const float* as = FP8 ? a.a_scale + t.row0 + row0 : nullptr;
+  const int rows = t.rows - row0;
+  tile.template store<u32x2>(
+      smem + (threadIdx.x >> 6) * WAVE_LDS,
+      [&](int row, int col, floatx4 v) {
+        if constexpr (FP8) {
+          if (ws) {
+            const float sa = row < rows ? as[row] : 0.0f;
+            const floatx4u sw = *reinterpret_cast<const floatx4u*>(ws + col);
 #pragma unroll
-  for (int i = 0; i < T::MB; ++i) {
-    const int row = T::row_of(i) + (lane & (T::M - 1));
-    const bool in = row < t.rows;
-    uint16_t* p = out + (int64_t)(t.row0 + row) * O + o0;
-    if constexpr (FP8) {
-      const float sa = ws && in ? a.a_scale[t.row0 + row] : 1.0f;
-      const int hi = lane >> 5;
-#pragma unroll
-      for (int j = 0; j < T::NB; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          u32x2 q[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            floatx4u sw{1.0f, 1.0f, 1.0f, 1.0f};
-            if (ws) sw = *reinterpret_cast<const floatx4u*>(ws + T::col_of(j) + 8 * (g + h) + 4 * hi);
-            float v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = tile.acc[i][j][4 * (g + h) + r] * (sa * sw[r]);
-            q[h] = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            for (int x = 0; x < 4; ++x) v[x] *= sa * sw[x];
           }
-          // the lower half wave's columns 8 (g + 1) .. + 3 against the upper half's 8 g + 4 .. + 7: a
-          // lane then has 8 consecutive columns, from 8 g in the lower and 8 (g + 1) in the upper half
-          const auto x = __builtin_amdgcn_permlane32_swap(q[0].x, q[1].x, false, false);
-          const auto y = __builtin_amdgcn_permlane32_swap(q[0].y, q[1].y, false, false);
-          if (in) st16(p + T::col_of(j) + 8 * (g + hi), u32x4{x[0], y[0], x[1], y[1]});
         }
-    } else {
-      const int q = lane >> 4;
-#pragma unroll
-      for (int j = 0; j < T::NB; j += 2) {
-        const floatx4 u = tile.acc[i][j], v = tile.acc[i][j + 1];
-        // odd 16-lane rows of block j against even ones of block j + 1: a lane then has 8 consecutive
-        // columns, of block j in even rows and of block j + 1 in odd ones
-        const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(u[0], u[1]), pack_bf16(v[0], v[1]), false, false);
-        const auto y = __builtin_amdgcn_permlane16_swap(pack_bf16(u[2], u[3]), pack_bf16(v[2], v[3]), false, false);
-        if (in) st16(p + T::col_of(j + (q & 1)) + 8 * (q >> 1), u32x4{x[0], y[0], x[1], y[1]});
-      }
-    }
-  }
+        return u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      },
+      [&](int row, int col, u32x4 q) {
+        if (row < rows) st16(out + (int64_t)row * O + col, q);
+      });
 }
 
 template <int MODE>

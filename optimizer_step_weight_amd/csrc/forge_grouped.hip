@@ -20,33 +20,52 @@ int launch_grouped_rows(int mode, const GroupedArgs& a, void* stream) {
   return (int)hipGetLastError();
 }
 
-__global__ __launch_bounds__(ml2::THREADS, kOcc2) void grouped_wgrad_kernel(GroupedWgradArgs a, float* dW) {
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[kSmem2];
-  grp::WTile t;
-  grp::wgrad_tile(a, t);
-  float* st = reinterpret_cast<float*>(smem);
-  if (t.half) {
-    ml2::floatx4 acc[4][4];
-    ml2::contract<Pipe2H>(acc, smem, t.g, t.n0, t.k0);
-    ml2::stage_acc_all(st, acc, 1.0f);
-    __syncthreads();
-    store_staged(st, dW, a.K, t.row0, t.k0);
-  } else {
-    ml2::floatx4 acc[8][4];
-    ml2::contract<Pipe2>(acc, smem, t.g, t.n0, t.k0);
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      ml2::stage_acc_half(st, acc, 1.0f, half);
-      __syncthreads();
-      store_staged(st, dW, a.K, t.row0 + half * ml2::EPI_ROWS, t.k0);
-      __syncthreads();
-    }
-  }
+namespace grp {
+
+// dW_e = dY_e^T X_e in fp32, 256 x 256 tiles of the contraction of forge_grouped.h (half as high or
+// wide at the end of an odd multiple of 128) over the group's rows alone: the operands' ranges begin
+// at the group's first row and end with its last, so a ragged end reads as zero.
+template <int HEIGHT, int WIDTH>
+__device__ __forceinline__ void wgrad_tile_f32(const GroupedWgradArgs& a, float* dW, int e, int start, int len, int n0,
+                                               int k0, unsigned char* smem) {
+  using A = Side<2, true, 64 * HEIGHT, true>;
+  using B = Side<2, true, 64 * WIDTH, true>;
+  using T = Tile<A, B>;
+  const int slabs = (len + 63) / 64;
+  Feed<A> fa;
+  Feed<B> fb;
+  fa.open(static_cast<const uint16_t*>(a.dY) + (int64_t)start * a.N + n0, (uint32_t)(len * a.N * 2 - n0 * 2),
+          (uint32_t)(a.N * 2), slabs);
+  fb.open(static_cast<const uint16_t*>(a.X) + (int64_t)start * a.K + k0, (uint32_t)(len * a.K * 2 - k0 * 2),
+          (uint32_t)(a.K * 2), slabs);
+  T tile;
+  tile.contract(smem, fa, fb, slabs);
+  barrier();  // every wave is done with the slabs
+  float* out = dW + ((int64_t)e * a.N + n0 + T::row0()) * a.K + k0 + T::col0();
+  tile.template store<floatx4>(
+      smem + (threadIdx.x >> 6) * WAVE_LDS, [](int, int, floatx4 v) { return v; },
+      [&](int row, int col, u32x4 q) { st16(out + (int64_t)row * a.K + col, q); });
 }
 
+__global__ __launch_bounds__(THREADS, 1) void grouped_wgrad_kernel(GroupedWgradArgs a, float* dW) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * 32768];
+  const int nbn = (int)((a.N + 255) / 256), nbk = (int)((a.K + 255) / 256), per = nbn * nbk;
+  const int e = (int)blockIdx.x / per, b = (int)blockIdx.x - e * per;
+  int start, len;
+  group_rows(a.ends, a.E, a.T, e, start, len);
+  const int n0 = 256 * (b % nbn), k0 = 256 * (b / nbn);
+  const bool low = a.N - n0 < 256, narrow = a.K - k0 < 256;
+  if (!low && !narrow) wgrad_tile_f32<4, 4>(a, dW, e, start, len, n0, k0, smem);
+  else if (!narrow) wgrad_tile_f32<2, 4>(a, dW, e, start, len, n0, k0, smem);
+  else if (!low) wgrad_tile_f32<4, 2>(a, dW, e, start, len, n0, k0, smem);
+  else wgrad_tile_f32<2, 2>(a, dW, e, start, len, n0, k0, smem);
+}
+
+}  // namespace grp
+
 int launch_grouped_wgrad(const GroupedWgradArgs& a, float* dW, void* stream) {
-  const dim3 grid((unsigned)(a.E * (int64_t)grp::wgrad_tiles(a.N, a.K)));
-  hipLaunchKernelGGL(grouped_wgrad_kernel, grid, dim3(ml2::THREADS), 0, (hipStream_t)stream, a, dW);
+  const dim3 grid((unsigned)(a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256)));
+  hipLaunchKernelGGL(grp::grouped_wgrad_kernel, grid, dim3(grp::THREADS), 0, (hipStream_t)stream, a, dW);
   return (int)hipGetLastError();
 }
 
