@@ -56,14 +56,30 @@ def _declare(L) -> None:
         getattr(L, f).restype = i64
 
 
-def _here(t: torch.Tensor, what: str) -> None:
-    if not t.is_cuda:
+# The smallest calls (a norm of one token, a step of a model's gains) take less time on the device
+# than their marshalling, so it asks a tensor for as little as it needs, and for the current device
+# once a call.
+_byref = ctypes.byref
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _here(t: torch.Tensor, what: str, dev: int) -> None:
+    at = t.get_device()
+    if at != dev:
+        if at < 0:
+            raise ValueError(f"{what} must be a CUDA tensor (got a {t.device} tensor)")
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _device(t: torch.Tensor, what: str) -> int:
+    """The current device, where t has to be."""
+    if t.get_device() < 0:   # asked first: without a GPU there is no current device
         raise ValueError(f"{what} must be a CUDA tensor (got a {t.device} tensor)")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _current_device()
 
 
-def _mat(t: Optional[torch.Tensor], what: str, scale: Optional[torch.Tensor] = None, scales: int = 0):
+def _mat(t: Optional[torch.Tensor], what: str, dev: int, scale: Optional[torch.Tensor] = None, scales: int = 0):
     """A descriptor of t as rows of its last dimension (1-D: one row), all leading dimensions
     flattened.  scale: a float32 tensor of `scales` elements (fp8 only)."""
     if t is None:
@@ -71,24 +87,32 @@ def _mat(t: Optional[torch.Tensor], what: str, scale: Optional[torch.Tensor] = N
     code = _CODE.get(t.dtype)
     if code is None:
         raise TypeError(f"{what}: unsupported dtype {t.dtype}")
-    _here(t, what)
-    if t.dim() < 1 or not t.is_contiguous():
+    if t.get_device() != dev:
+        _here(t, what, dev)
+    shape = t.shape
+    if not shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    cols = t.shape[-1]
-    rows = t.numel() // cols if cols else 0
+    cols = shape[-1]
+    rows = shape[0] if len(shape) == 2 else t.numel() // cols if cols else 0
+    at = None
     if scale is not None:
         if code != FP8_E4M3:
             raise ValueError(f"{what}: a {t.dtype} tensor takes no scale")
-        _vec(scale, f"the scale of {what}", scales)
-    return Tensor(t.data_ptr(), code, rows, cols, cols, None if scale is None else scale.data_ptr())
+        at = _vec(scale, f"the scale of {what}", scales, dev)
+    return Tensor(t.data_ptr(), code, rows, cols, cols, at)
 
 
-def _vec(t: torch.Tensor, what: str, n: int, dtype=torch.float32) -> int:
+def _vec(t: torch.Tensor, what: str, n: int, dev: int, dtype=torch.float32) -> int:
     """Address of a contiguous vector of n elements."""
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements (got {t.dtype}, {t.numel()})")
-    _here(t, what)
+    if t.get_device() != dev:
+        _here(t, what, dev)
     return t.data_ptr()
+
+
+def _stream(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else int(stream)
 
 
 def rmsnorm(x, gain, y, *, residual=None, h=None, rstd=None, y_scale=None, amax=None, eps: float = 1e-6,
@@ -99,13 +123,14 @@ def rmsnorm(x, gain, y, *, residual=None, h=None, rstd=None, y_scale=None, amax=
     row, float32) is what the backward pass takes; amax (one float32) is raised to max |y|."""
     if scale_mode not in SCALE_MODE:
         raise ValueError(f"scale_mode must be 'row' or 'tensor' (got {scale_mode!r})")
-    X = _mat(x, "x")
+    dev = _device(x, "x")
+    X = _mat(x, "x", dev)
     rows = X.rows
     _check(_lib().forge_rmsnorm(
-        _ref(X), _ref(_mat(residual, "residual")), _ref(_mat(gain, "gain")), eps, _ref(_mat(h, "h")),
-        _ref(_mat(y, "y", y_scale, rows if scale_mode == "row" else 1)), SCALE_MODE[scale_mode],
-        None if rstd is None else _vec(rstd, "rstd", rows), None if amax is None else _vec(amax, "amax", 1),
-        _stream(stream)))
+        _byref(X), _ref(_mat(residual, "residual", dev)), _byref(_mat(gain, "gain", dev)), eps, _ref(_mat(h, "h", dev)),
+        _byref(_mat(y, "y", dev, y_scale, rows if scale_mode == "row" else 1)), SCALE_MODE[scale_mode],
+        None if rstd is None else _vec(rstd, "rstd", rows, dev),
+        None if amax is None else _vec(amax, "amax", 1, dev), _stream(stream, dev)))
 
 
 def rmsnorm_backward_workspace(rows: int, width: int, device="cuda") -> torch.Tensor:
@@ -120,51 +145,56 @@ def rmsnorm_backward(dy, h, gain, rstd, dx, dgain=None, *, dh=None, workspace=No
     """dx (of x and of residual; dh, the gradient arriving on h itself, is added) and dgain
     (float32, overwritten) of rmsnorm (forge_rmsnorm_backward).  A workspace is allocated where
     dgain is wanted and none is given."""
-    H = _mat(h, "h")
+    dev = _device(h, "h")
+    H = _mat(h, "h", dev)
     rows, width = H.rows, H.cols
     if dgain is not None and workspace is None:
         workspace = rmsnorm_backward_workspace(rows, width, h.device)
     if workspace is not None:
-        _here(workspace, "workspace")
+        _here(workspace, "workspace", dev)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     _check(_lib().forge_rmsnorm_backward(
-        _ref(_mat(dy, "dy")), _ref(_mat(dh, "dh")), _ref(H), _ref(_mat(gain, "gain")), _vec(rstd, "rstd", rows),
-        _ref(_mat(dx, "dx")), _ref(_mat(dgain, "dgain")), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        _byref(_mat(dy, "dy", dev)), _ref(_mat(dh, "dh", dev)), _byref(H), _byref(_mat(gain, "gain", dev)),
+        _vec(rstd, "rstd", rows, dev), _byref(_mat(dx, "dx", dev)), _ref(_mat(dgain, "dgain", dev)),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream, dev)))
 
 
-def _groups(ends, W, what="W"):
+def _groups(ends, dev, W, what="W"):
     """(address of ends, number of groups); W [groups, N, K] where it is given."""
     n = ends.numel()
     if W is not None and (W.dim() != 3 or W.shape[0] != n):
         raise ValueError(f"{what} must be [experts, N, K] with one expert for each of the {n} ends "
                          f"(got {tuple(W.shape)})")
-    return _vec(ends, "ends", n, torch.int32), n
+    return _vec(ends, "ends", n, dev, torch.int32), n
 
 
 def grouped_gemm(X, W, ends, Y, *, x_scale=None, w_scale=None, stream=None) -> None:
     """Y[t] = X[t] W[e]^T for the rows t of group e (forge_grouped_gemm).  X [T, K] sorted by expert,
     W [E, N, K], ends [E] int32 on the device: the first row after each group.  bfloat16, or
     float8_e4m3fn X and W with x_scale [T] and w_scale [E, N]; Y [T, N] bfloat16."""
-    at, n = _groups(ends, W)
-    _check(_lib().forge_grouped_gemm(_ref(_mat(X, "X", x_scale, X.numel() // X.shape[-1])),
-                                     _ref(_mat(W, "W", w_scale, n * W.shape[1])), at, n, _ref(_mat(Y, "Y")),
-                                     _stream(stream)))
+    dev = _device(X, "X")
+    at, n = _groups(ends, dev, W)
+    _check(_lib().forge_grouped_gemm(_byref(_mat(X, "X", dev, x_scale, X.numel() // X.shape[-1])),
+                                     _byref(_mat(W, "W", dev, w_scale, n * W.shape[1])), at, n,
+                                     _byref(_mat(Y, "Y", dev)), _stream(stream, dev)))
 
 
 def grouped_dgrad(dY, W, ends, dX, *, stream=None) -> None:
     """dX[t] = dY[t] W[e] for the rows t of group e (forge_grouped_dgrad)."""
-    at, n = _groups(ends, W)
-    _check(_lib().forge_grouped_dgrad(_ref(_mat(dY, "dY")), _ref(_mat(W, "W")), at, n, _ref(_mat(dX, "dX")),
-                                      _stream(stream)))
+    dev = _device(dY, "dY")
+    at, n = _groups(ends, dev, W)
+    _check(_lib().forge_grouped_dgrad(_byref(_mat(dY, "dY", dev)), _byref(_mat(W, "W", dev)), at, n,
+                                      _byref(_mat(dX, "dX", dev)), _stream(stream, dev)))
 
 
 def grouped_wgrad(X, dY, ends, dW, *, stream=None) -> None:
     """dW[e] = dY_e^T X_e in float32 for every group (forge_grouped_wgrad)."""
-    at, n = _groups(ends, dW, "dW")
-    _check(_lib().forge_grouped_wgrad(_ref(_mat(X, "X")), _ref(_mat(dY, "dY")), at, n, _ref(_mat(dW, "dW")),
-                                      _stream(stream)))
+    dev = _device(X, "X")
+    at, n = _groups(ends, dev, dW, "dW")
+    _check(_lib().forge_grouped_wgrad(_byref(_mat(X, "X", dev)), _byref(_mat(dY, "dY", dev)), at, n,
+                                      _byref(_mat(dW, "dW", dev)), _stream(stream, dev)))
 
 
 def grouped_wgrad_step(X, dY, ends, W, m=None, v=None, *, opt="adamw", hyper=None, step: int, seed: int,
@@ -172,13 +202,17 @@ def grouped_wgrad_step(X, dY, ends, W, m=None, v=None, *, opt="adamw", hyper=Non
                        stream=None) -> None:
     """The fused step of every expert's weight: W [E, N, K], m, v updated in place from
     dW[e] = dY_e^T X_e (forge_grouped_wgrad_step; arguments as wgrad_step)."""
-    at, n = _groups(ends, W)
+    dev = _device(X, "X")
+    at, n = _groups(ends, dev, W)
     dyn = _dyn(state_map)
     flat = lambda t: None if t is None else t.view(-1, t.shape[-1])  # noqa: E731
     _check(_lib().forge_grouped_wgrad_step(
-        _ref(_mat(X, "X")), _ref(_mat(dY, "dY")), at, n, _ref(_mat(W, "W")), _ref(_tensor(flat(m), m_scale, dyn)),
-        _ref(_tensor(flat(v), v_scale, dyn)), ctypes.byref(_hyper(hyper)), _opt(opt), int(step),
-        int(seed) & 0xFFFFFFFFFFFFFFFF, _ref(_opts(w_preround_out, sr, W)), _stream(stream)))
+        _byref(_mat(X, "X", dev)), _byref(_mat(dY, "dY", dev)), at, n, _byref(_mat(W, "W", dev)),
+        _ref(_tensor(flat(m), m_scale, dyn)), _ref(_tensor(flat(v), v_scale, dyn)), _byref(_hyper(hyper)), _opt(opt),
+        int(step), int(seed) & 0xFFFFFFFFFFFFFFFF, _ref(_opts(w_preround_out, sr, W)), _stream(stream, dev)))
+
+
+_NO_SR = _byref(StepOpts(None, 0))
 
 
 class MultiStep:
@@ -235,6 +269,7 @@ class MultiStep:
             if L[name + "_scale"] is None and codes[name] != F32:
                 raise ValueError(f"8-bit {name} needs {name}_scale")
         entries = (_MultiTensor * n)()
+        dev = _device(L["W"][0], "W[0]") if n else -1
         for i, w in enumerate(L["W"]):
             count = w.numel()
             e = entries[i]
@@ -245,21 +280,21 @@ class MultiStep:
                 t = L[name][i]
                 if name in ("W", "g") and t.dtype not in (torch.float32, torch.bfloat16):
                     raise TypeError(f"{name}[{i}]: unsupported dtype {t.dtype}")
-                setattr(e, name, _vec(t, f"{name}[{i}]", count, t.dtype) or None)
+                setattr(e, name, _vec(t, f"{name}[{i}]", count, dev, t.dtype) or None)
             e.w_dtype, e.g_dtype = _CODE[w.dtype], _CODE[L["g"][i].dtype]
             for name in ("m_scale", "v_scale"):
                 if L[name] is not None:
-                    setattr(e, name, _vec(L[name][i], f"{name}[{i}]", -(-count // 64)) or None)
+                    setattr(e, name, _vec(L[name][i], f"{name}[{i}]", -(-count // 64), dev) or None)
         lib = _lib()
         size = lib.forge_multi_table_bytes(entries, n)
         host = torch.empty(max(size, 16), dtype=torch.uint8)
         self._info = _MultiInfo()
         _check(lib.forge_multi_pack(entries, n, self.opt, codes["m"], codes["v"], host.data_ptr(), host.numel(),
                                     ctypes.byref(self._info)))
-        self._hypers = (Hyper * 8)()
+        self._hypers, self._given = (Hyper * 8)(), None
         if n:
-            self._device = L["W"][0].device
-            self._table = host.to(self._device)   # a synchronous copy: the table is there for any stream
+            self._device = dev
+            self._table = host.to(L["W"][0].device)   # a synchronous copy: the table is there for any stream
 
     def step(self, *, step: int, hyper=None, grad_scale: Optional[torch.Tensor] = None, sr: bool = True,
              stream=None) -> None:
@@ -268,16 +303,20 @@ class MultiStep:
         hypers = list(hyper) if isinstance(hyper, (list, tuple)) else [hyper if hyper is not None else {}]
         if len(hypers) > 8:
             raise ValueError("at most 8 groups of hyper-parameters")
-        for i, h in enumerate(hypers):
-            self._hypers[i] = _hyper(h)
-        if self._device is not None and self._device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {self._device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        opts = None if sr else StepOpts(None, 0)
+        if self._given is None or self._given != hypers:   # by value: they seldom change from step to step
+            for i, h in enumerate(hypers):
+                self._hypers[i] = _hyper(h)
+            self._given = [dict(h) for h in hypers] if all(isinstance(h, dict) for h in hypers) else None
+        dev = self._device
+        table = None
+        if dev is not None:
+            if dev != _current_device():
+                raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
+            table = self._table.data_ptr()
         _check(_lib().forge_multi_step(
-            ctypes.byref(self._info), self._table.data_ptr() if self._device is not None else None, self._hypers,
-            len(hypers), int(step), None if grad_scale is None else _vec(grad_scale, "grad_scale", 1), _ref(opts),
-            _stream(stream)))
+            _byref(self._info), table, self._hypers, len(hypers), int(step),
+            None if grad_scale is None else _vec(grad_scale, "grad_scale", 1, dev),
+            None if sr else _NO_SR, None if dev is None else _stream(stream, dev)))
 
 
 # the C ABI names
