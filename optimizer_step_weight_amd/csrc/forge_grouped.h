@@ -69,11 +69,19 @@ struct RowTile {
   int row0;       // first row
   int rows;       // rows of this tile, 1 .. BM
   int n;          // column tile
+  int cols;       // columns of a column tile
 };
 
-// The tile of workgroup b among the row tiles of BM rows x nbn column tiles; false: none left.
+// Up to this many tiles of 256 columns, the tiles take 128, all still on CUs at once: a product of
+// few rows is a pass over the live experts' weights, and wants many CUs to read.  Experts of 1024 x
+// 2048 in bf16: 30 live ones 29.3 us in 120 wide tiles, 26.0 us in 240 narrow ones (4.8 TB/s); 39 live
+// ones 38.5 us in 156 wide tiles, 50.9 us in 312 narrow ones.
+constexpr int NARROW_TILES = 128;
+
+// The tile of workgroup b among the row tiles of BM rows x the column tiles of O columns, of 256
+// columns or, where there are few tiles and `least` is 128, of 128; false: none left.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T, int nbn, int b, RowTile& out) {
+__device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T, int64_t O, int least, int b, RowTile& out) {
   const int lane = (int)(threadIdx.x & 63), chunks = E / 64 + 1;
   auto tiles_of = [&](const Chunk& k) { return (int)((k.end - k.start + BM - 1) / BM); };
   auto scan = [&](int v) {
@@ -94,6 +102,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T,
     total += __builtin_amdgcn_readlane(incl, 63);
     carry = __builtin_amdgcn_readlane((int)k.end, 63);
   }
+  const int wide = (int)((O + 255) / 256);
+  out.cols = least < 256 && (int64_t)total * wide <= NARROW_TILES ? 128 : 256;
+  const int nbn = out.cols < 256 ? (int)((O + 127) / 128) : wide;
   total *= nbn;
   if (b >= total) return false;
   const int t = xcd_run(b, total);
@@ -503,7 +514,7 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, const RowTile& t
   using A = Side<ESZ, false, 64 * HEIGHT>;
   using B = Side<ESZ, NN, 64 * WIDTH>;
   using T = Tile<A, B>;
-  const int64_t C = NN ? a.N : a.K, O = NN ? a.K : a.N, o0 = (int64_t)t.n * 256;
+  const int64_t C = NN ? a.N : a.K, O = NN ? a.K : a.N, o0 = (int64_t)t.n * t.cols;
   const int slabs = t.e < a.E ? (int)(C * ESZ / 128) : 0;  // rows of no group: zeros
   Feed<A> fa;
   Feed<B> fb;
@@ -544,8 +555,8 @@ __global__ __launch_bounds__(THREADS, 1) void grouped_rows_kernel(GroupedArgs a)
   __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * 32768];
   const int64_t O = MODE == FORGE_GROUPED_NN ? a.K : a.N;
   RowTile t;
-  if (!find_tile<256>(a.ends, a.E, a.T, (int)((O + 255) / 256), (int)blockIdx.x, t)) return;
-  const bool narrow = O - (int64_t)t.n * 256 < 256;
+  if (!find_tile<256>(a.ends, a.E, a.T, O, a.cols, (int)blockIdx.x, t)) return;
+  const bool narrow = t.cols < 256 || O - (int64_t)t.n * 256 < 256;
   switch ((t.rows + 63) / 64 + (narrow ? 4 : 0)) {
     case 1: rows_tile<MODE, 1, 4>(a, t, smem); break;
     case 2: rows_tile<MODE, 2, 4>(a, t, smem); break;

@@ -6,9 +6,13 @@
 
 namespace forge {
 
-int launch_grouped_rows(int mode, const GroupedArgs& a, void* stream) {
+int launch_grouped_rows(int mode, const GroupedArgs& given, void* stream) {
+  GroupedArgs a = given;
   const int64_t O = mode == FORGE_GROUPED_NN ? a.K : a.N;
-  const int64_t tiles = (a.T / 256 + (a.E < a.T ? a.E : a.T) + 1) * ((O + 255) / 256);
+  const int64_t row_tiles = a.T / 256 + (a.E < a.T ? a.E : a.T) + 1;
+  // the device, which knows the groups, takes the narrow tiles if even the fewest there can be fit
+  a.cols = a.T / 256 * ((O + 255) / 256) <= grp::NARROW_TILES ? 128 : 256;
+  const int64_t tiles = row_tiles * ((O + a.cols - 1) / a.cols);
   const dim3 grid((unsigned)tiles), block(grp::THREADS);
   hipStream_t st = (hipStream_t)stream;
   switch (mode) {

@@ -55,6 +55,7 @@ struct GroupedArgs {
   const float* w_scale;
   const int32_t* ends;
   int32_t E;
+  int32_t cols;          // least output columns of a tile: 256 or 128
   int64_t T, N, K;
 };
 enum : int { FORGE_GROUPED_NT = 0, FORGE_GROUPED_NN = 1, FORGE_GROUPED_NT8 = 2 };
