@@ -29,6 +29,26 @@ __device__ __forceinline__ int xcd_run(int b, int total) {
   return (x < rem ? x * (per + 1) : rem * (per + 1) + (x - rem) * per) + loc;
 }
 
+// Inclusive scans over the wave by data-parallel moves within the vector unit: a workgroup finds its
+// tile before it can load anything, and shuffles through LDS took 1.3 of the 3.4 thousand cycles.
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F&& join) {
+  // lanes without a source take 0, which both joins leave as it is (no value is negative)
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // 1, 2, 4, 8 lanes up in a row of 16
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // last lane of a row to the next row
+  v = join(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // lane 31 to the upper half
+  return v;
+}
+__device__ __forceinline__ int scan_max(int v) {
+  return wave_scan(v, [](int a, int b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ int scan_sum(int v) {
+  return wave_scan(v, [](int a, int b) { return a + b; });
+}
+
 // The groups' ends, 64 at a time: lane l of the wave holds group 64 c + l.  Ends are clamped to
 // [0, T] and made ascending (a running maximum), so whatever the device holds, the groups cover
 // disjoint ranges of rows in bounds.  Group E holds the rows after the last end.
@@ -40,11 +60,7 @@ __device__ __forceinline__ Chunk load_chunk(const int32_t* ends, int E, int64_t 
   int64_t v = e < E ? (int64_t)ends[e] : (e == E ? T : 0);
   v = v < 0 ? 0 : (v > T ? T : v);
   if (lane == 0 && v < carry) v = carry;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up((int)v, o);
-    if (lane >= o && up > v) v = up;
-  }
+  v = scan_max((int)v);
   const int prev = __shfl_up((int)v, 1);
   Chunk k;
   k.end = v;
@@ -82,23 +98,15 @@ constexpr int NARROW_TILES = 128;
 // columns or, where there are few tiles and `least` is 128, of 128; false: none left.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T, int64_t O, int least, int b, RowTile& out) {
-  const int lane = (int)(threadIdx.x & 63), chunks = E / 64 + 1;
+  const int chunks = E / 64 + 1;
   auto tiles_of = [&](const Chunk& k) { return (int)((k.end - k.start + BM - 1) / BM); };
-  auto scan = [&](int v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(v, o);
-      if (lane >= o) v += up;
-    }
-    return v;
-  };
   int64_t carry = 0;
   int total = 0;  // the host keeps the grid, and with it every tile number, below 2^31
   Chunk k{};
   int incl = 0;
   for (int c = 0; c < chunks; ++c) {
     k = load_chunk(ends, E, T, c, carry);
-    incl = scan(tiles_of(k));
+    incl = scan_sum(tiles_of(k));
     total += __builtin_amdgcn_readlane(incl, 63);
     carry = __builtin_amdgcn_readlane((int)k.end, 63);
   }
@@ -113,7 +121,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T,
   for (int c = 0; c < chunks; ++c) {
     if (chunks > 1) {
       k = load_chunk(ends, E, T, c, carry);
-      incl = scan(tiles_of(k));
+      incl = scan_sum(tiles_of(k));
       carry = __builtin_amdgcn_readlane((int)k.end, 63);
     }
     const uint64_t past = __ballot((before + incl) * nbn > t);
@@ -122,8 +130,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* ends, int E, int64_t T,
       continue;
     }
     const int l = __builtin_ctzll(past);
-    const int cnt = __shfl(tiles_of(k), l), last = __shfl(incl, l);
-    const int start = __shfl((int)k.start, l), end = __shfl((int)k.end, l);
+    const int cnt = __builtin_amdgcn_readlane(tiles_of(k), l), last = __builtin_amdgcn_readlane(incl, l);
+    const int start = __builtin_amdgcn_readlane((int)k.start, l), end = __builtin_amdgcn_readlane((int)k.end, l);
     const int local = t - (before + last - cnt) * nbn;
     // blocks of G row tiles, row tiles fastest
     constexpr int G = 8;
@@ -293,6 +301,8 @@ struct View {
   }
 };
 
+constexpr int WAVE_LDS = 32768;  // of the tile's 160 KiB, once they are free
+
 template <class A, class B>  // second (rows), first (columns)
 struct Tile {
   static constexpr int MB = A::BLOCKS, NB = B::BLOCKS, ESZ = A::ESZ, M = A::M;
@@ -461,8 +471,8 @@ struct Tile {
   static __device__ __forceinline__ int col0() { return M * NB * (int)((threadIdx.x >> 6) & 1); }
 
   // The tile to memory by rows.  A lane holds 4 consecutive columns of one of a block's M rows, and a
-  // store from there would touch 16 rows at once, 32 or 64 bytes of each.  So the M rows of a row of
-  // blocks pass through 8 KiB of the wave's own in LDS (no barrier: a wave's LDS accesses are in
+  // store from there would touch 16 rows at once, 32 or 64 bytes of each.  So rows of blocks pass, some
+  // at a time, through 32 KiB of the wave's own in LDS (no barrier: a wave's LDS accesses are in
   // order), and leave as whole rows of the wave's M NB columns, 16 bytes a lane.  Chunks of 16 bytes
   // are XOR-swizzled with the row.  pack(row, column, v): the 4 values of a row of the wave from that
   // column on as they are stored (8 bytes bf16 or 16 fp32); put(row, column, q): stores 16 bytes.
@@ -471,32 +481,35 @@ struct Tile {
     constexpr int SIZE = sizeof(Unit) / 4;              // of an element
     constexpr int ROW = M * NB * SIZE, CH = ROW / 16;   // bytes and chunks of a row
     constexpr int MASK = (CH < 16 ? CH : 16) - 1;
+    constexpr int FIT = WAVE_LDS / (M * ROW), G = FIT < MB ? FIT : MB;  // rows of blocks at a time
     const int lane = (int)threadIdx.x & 63, row = lane & (M - 1);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
+    for (int i0 = 0; i0 < MB; i0 += G) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
+      for (int i = i0; i < (i0 + G < MB ? i0 + G : MB); ++i)
 #pragma unroll
-        for (int g = 0; g < M * M / 256; ++g) {
-          const int c4 = M / 4 * j + 64 / M * g + lane / M;  // column / 4
-          const Unit u = pack(M * i + row, 4 * c4, floatx4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                                                           acc[i][j][4 * g + 3]});
-          const int byte = c4 * (int)sizeof(Unit);
-          *reinterpret_cast<Unit*>(wave_lds + row * ROW + 16 * ((byte >> 4) ^ (row & MASK)) + (byte & 15)) = u;
-        }
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int g = 0; g < M * M / 256; ++g) {
+            const int c4 = M / 4 * j + 64 / M * g + lane / M;  // column / 4
+            const Unit u = pack(M * i + row, 4 * c4, floatx4{acc[i][j][4 * g], acc[i][j][4 * g + 1],
+                                                             acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
+            const int byte = c4 * (int)sizeof(Unit);
+            *reinterpret_cast<Unit*>(wave_lds + ((i - i0) * M + row) * ROW + 16 * ((byte >> 4) ^ (row & MASK)) +
+                                     (byte & 15)) = u;
+          }
       __builtin_amdgcn_wave_barrier();
       asm volatile("" ::: "memory");
 #pragma unroll
-      for (int t = 0; t < M * CH / 64; ++t) {
+      for (int t = 0; t < (i0 + G < MB ? G : MB - i0) * M * CH / 64; ++t) {
         const int p = lane + 64 * t, r = p / CH, c = p % CH;
-        put(M * i + r, 16 / SIZE * c, *reinterpret_cast<const u32x4*>(wave_lds + r * ROW + 16 * (c ^ (r & MASK))));
+        put(M * i0 + r, 16 / SIZE * c, *reinterpret_cast<const u32x4*>(wave_lds + r * ROW + 16 * (c ^ (r & MASK))));
       }
       __builtin_amdgcn_wave_barrier();
       asm volatile("" ::: "memory");
     }
   }
 };
-constexpr int WAVE_LDS = 8192;
 
 // Two values to bf16, nearest even, in one instruction.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
