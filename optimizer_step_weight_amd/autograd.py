@@ -1,4 +1,5 @@
-"""PyTorch autograd integration: a linear layer whose backward pass updates its own weight.
+"""PyTorch autograd integration: layers whose backward pass updates their own weight (`FusedLinear`,
+and `FusedExperts` over the experts of a mixture), and the RMS norm before them (`RMSNorm`).
 
 FORGE explainer (gist.science), Technical Summary section 2 "Core Mechanism": the weight
 gradient of a layer is consumed tile by tile by the optimizer and never stored.  In a PyTorch
@@ -21,7 +22,8 @@ from typing import Optional
 
 import torch
 
-from . import linear_backward_step, wgrad_step
+from . import (grouped_dgrad, grouped_gemm, grouped_wgrad_step, linear_backward_step, rmsnorm, rmsnorm_backward,
+               wgrad_step)
 
 _STATES = {"adamw": "mv", "nadam": "mv", "radam": "mv", "lion": "m", "rmsprop": "v", "adagrad": "v",
            "sgd": "", "sgd_momentum": "m"}
@@ -114,3 +116,110 @@ class FusedLinear(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, opt={self.opt}"
+
+
+class _ExpertsStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x2d, anchor, ends, layer):
+        ctx.layer = layer
+        ctx.save_for_backward(x2d, ends)
+        y = torch.empty(x2d.shape[0], layer.out_features, dtype=torch.bfloat16, device=x2d.device)
+        grouped_gemm(x2d, layer.weight, ends, y)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2d, ends = ctx.saved_tensors
+        layer = ctx.layer
+        dy = dy.contiguous().to(torch.bfloat16)
+        layer.step_count += 1
+        dx = None
+        if ctx.needs_input_grad[0]:   # with the weights as they were
+            dx = torch.empty_like(x2d)
+            grouped_dgrad(dy, layer.weight, ends, dx)
+        grouped_wgrad_step(x2d, dy, ends, layer.weight, layer.m, layer.v, opt=layer.opt, hyper=layer.hyper,
+                           step=layer.step_count, seed=layer.seed, m_scale=layer.m_scale, v_scale=layer.v_scale)
+        return dx, None, None, None
+
+
+class FusedExperts(FusedLinear):
+    """y[t] = x[t] W[e]^T for the rows t of expert e: FusedLinear over `experts` weights
+    [experts, out_features, in_features], whose backward updates every expert's weight (one without
+    rows takes a step with a zero gradient).  forward(x, ends): the rows of x are sorted by expert,
+    ends[e] (int32, on the device) is the first row after expert e.  The other arguments, the limits
+    and one backward for each forward are FusedLinear's."""
+
+    def __init__(self, experts: int, in_features: int, out_features: int, *, opt: str = "adamw", hyper=None,
+                 state_dtype: str = "f32", seed: int = 0, weight: Optional[torch.Tensor] = None, device="cuda"):
+        if weight is not None:
+            if tuple(weight.shape) != (experts, out_features, in_features):
+                raise ValueError(f"weight must be [{experts}, {out_features}, {in_features}] (got {tuple(weight.shape)})")
+            weight = weight.reshape(-1, in_features)
+        if out_features % 128:
+            raise ValueError("in_features and out_features must be multiples of 128")
+        scale = 1.0 / in_features ** 0.5
+        if weight is None:
+            weight = torch.randn(experts * out_features, in_features, device=device) * scale
+        super().__init__(in_features, experts * out_features, opt=opt, hyper=hyper, state_dtype=state_dtype, seed=seed,
+                         weight=weight, device=device)
+        self.experts, self.out_features = int(experts), out_features
+        shape = (experts, out_features, in_features)
+        for name in ("weight", "m", "v"):
+            if getattr(self, name) is not None:
+                setattr(self, name, getattr(self, name).view(shape))
+
+    def forward(self, x: torch.Tensor, ends: torch.Tensor) -> torch.Tensor:
+        if x.dim() != 2 or x.shape[1] != self.in_features:
+            raise ValueError(f"x must be [rows, {self.in_features}] (got {tuple(x.shape)})")
+        if ends.numel() != self.experts:
+            raise ValueError(f"ends must have {self.experts} entries (got {ends.numel()})")
+        return _ExpertsStep.apply(x.to(torch.bfloat16).contiguous(), self._anchor, ends, self)
+
+    def extra_repr(self) -> str:
+        return f"experts={self.experts}, " + super().extra_repr()
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gain, eps):
+        h = None if residual is None else torch.empty_like(x)
+        y = torch.empty_like(x)
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        rmsnorm(x, gain, y, residual=residual, h=h, rstd=rstd, eps=eps)
+        ctx.save_for_backward(x if h is None else h, gain, rstd)
+        ctx.alone = h is None
+        ctx.set_materialize_grads(False)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, gain, rstd = ctx.saved_tensors
+        if dy is None:   # only the stream was used
+            return dh, dh, None, None
+        dx = torch.empty_like(h)
+        dgain = torch.empty(gain.shape, dtype=torch.float32, device=h.device) if ctx.needs_input_grad[2] else None
+        rmsnorm_backward(dy.contiguous(), h, gain, rstd, dx, dgain, dh=None if dh is None else dh.contiguous())
+        return dx, None if ctx.alone else dx, None if dgain is None else dgain.to(gain.dtype), None
+
+
+class RMSNorm(torch.nn.Module):
+    """y = h / sqrt(mean(h^2) + eps) * gain over the last dimension (float32 or bfloat16), with h = x.
+    With a residual of the same shape h = x + residual, rounded to their dtype, and forward returns
+    (y, h): h goes on as the residual stream.  gain is an ordinary parameter (float32)."""
+
+    def __init__(self, width: int, *, eps: float = 1e-6, device="cuda"):
+        super().__init__()
+        self.width, self.eps = int(width), float(eps)
+        self.gain = torch.nn.Parameter(torch.ones(width, device=device))
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
+        if x.shape[-1] != self.width:
+            raise ValueError(f"expected last dimension {self.width}, got {x.shape[-1]}")
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+            raise ValueError("residual must have the shape and dtype of x")
+        flat = lambda t: t.reshape(-1, self.width).contiguous()  # noqa: E731
+        out = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), self.gain, self.eps)
+        return out.view(x.shape) if residual is None else tuple(t.view(x.shape) for t in out)
+
+    def extra_repr(self) -> str:
+        return f"width={self.width}, eps={self.eps}"

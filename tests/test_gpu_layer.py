@@ -496,3 +496,70 @@ def test_layer_step_in_a_graph(lib):
         torch.cuda.synchronize()
         for k in a:
             assert k == "ws" or torch.equal(a[k], c[k]), k
+
+
+# ------------------------------------------------------------------ every tile of the products
+def _exact_products(lib, ends, T, N, K, E):
+    X, dY, W = ints((T, K), 4, 11), ints((T, N), 4, 12), ints((E, N, K), 4, 13)
+    ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    Y, dX = torch.full((T, N), float("nan"), dtype=BF, device="cuda"), torch.full((T, K), float("nan"), dtype=BF, device="cuda")
+    want = R.grouped(X, W, ends, True)[0].to(BF)
+    lib.grouped_gemm(X.cuda(), W.cuda(), ed, Y)
+    assert torch.equal(Y.cpu(), want)
+    lib.grouped_dgrad(dY.cuda(), W.cuda(), ed, dX)
+    assert torch.equal(dX.cpu(), R.grouped(dY, W, ends, False)[0].to(BF))
+    xs, ws = torch.ones(T, device="cuda"), torch.ones(E, N, device="cuda")
+    lib.grouped_gemm(X.cuda().to(FP8), W.cuda().to(FP8), ed, Y.fill_(float("nan")), x_scale=xs, w_scale=ws)
+    assert torch.equal(Y.cpu(), want)
+
+
+# rows of a group: every height of a tile (64, 128, 192, 256), one row more and one less
+HEIGHTS = [1, 63, 64, 65, 128, 129, 191, 192, 193, 0, 255, 256, 257, 700]
+HEIGHT_ENDS = [sum(HEIGHTS[:i + 1]) for i in range(len(HEIGHTS))]
+
+
+@pytest.mark.parametrize("N,K", [(1280, 128), (1408, 256), (128, 1408), (256, 1280), (1408, 384), (640, 1408)])
+def test_grouped_wide_tiles_exact(lib, N, K):
+    """More than 128 tiles of 256 columns in the forward (N) or the input gradient (K): every height
+    and width of a tile, over one slab of the contraction and more."""
+    T = HEIGHT_ENDS[-1] + 3
+    _exact_products(lib, HEIGHT_ENDS, T, N, K, len(HEIGHTS))
+    # twice as many groups, so that one of the two products has the wide tiles for certain
+    ends = HEIGHT_ENDS + [HEIGHT_ENDS[-1] + e for e in HEIGHT_ENDS]
+    _exact_products(lib, ends, 2 * HEIGHT_ENDS[-1], N, K, 2 * len(HEIGHTS))
+
+
+@pytest.mark.parametrize("slabs", [1, 2, 3, 4, 5, 7])
+def test_grouped_contraction_lengths_exact(lib, slabs):
+    """Contractions of 1 to 14 slabs (128 elements a step: 2 bf16 slabs, 1 fp8 slab)."""
+    _exact_products(lib, [150, 500], 500, 128 * slabs, 128 * slabs, 2)
+
+
+@pytest.mark.parametrize("N,K", [(128, 128), (256, 384), (384, 256), (512, 512)])
+def test_grouped_wgrad_rows_exact(lib, N, K):
+    """Groups of 0 to 5 slabs of 64 rows, ragged ends, all four tile shapes."""
+    rows = [0, 1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 192, 193, 300]
+    ends = [sum(rows[:i + 1]) for i in range(len(rows))]
+    T = ends[-1]
+    X, dY = ints((T, K), 4, 21), ints((T, N), 4, 22)
+    dW = torch.full((len(rows), N, K), float("nan"), device="cuda")
+    lib.grouped_wgrad(X.cuda(), dY.cuda(), torch.tensor(ends, dtype=torch.int32, device="cuda"), dW)
+    assert torch.equal(dW.cpu(), R.grouped_wgrad(X, dY, ends).float())
+
+
+def test_grouped_products_repeat_bit_for_bit(lib):
+    """The same inputs give the same bits, call after call and on another stream."""
+    g = gen(9)
+    T, E, N, K = 900, 4, 1408, 640
+    X, W = torch.randn(T, K, generator=g).to(BF).cuda(), torch.randn(E, N, K, generator=g).to(BF).cuda()
+    ends = torch.tensor([100, 400, 400, 880], dtype=torch.int32, device="cuda")
+    Y = torch.empty(T, N, dtype=BF, device="cuda")
+    lib.grouped_gemm(X, W, ends, Y)
+    first = Y.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            lib.grouped_gemm(X, W, ends, Y)
+    s.synchronize()
+    assert torch.equal(Y, first)
