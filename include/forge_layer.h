@@ -42,8 +42,7 @@ extern "C" {
  *   rstd             T fp32 or NULL.
  *   amax             one fp32 or NULL: raised to max |y| over the tensor where that is larger
  *                    (the caller sets it to 0 first; NaN sticks), for the next tensor scale.
- * D is any length >= 1; rows whose bytes are a multiple of 16 (D % 8 == 0) and D <= 16384 take one
- * pass over memory.  T D < 2^48 / 4.
+ * D is any length >= 1; rows of D <= 16384 take one pass over memory, fastest where D % 8 == 0.  T D < 2^48 / 4.
  */
 forge_status forge_rmsnorm(const forge_tensor* x, const forge_tensor* residual, const forge_tensor* gain, float eps,
                            forge_tensor* h, forge_tensor* y, int32_t scale_mode, float* rstd, float* amax,

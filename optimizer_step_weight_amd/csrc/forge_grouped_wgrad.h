@@ -1,12 +1,15 @@
-// forge_grouped_wgrad.h -- dW_e = dY_e^T X_e of every expert on the LDS-DMA path of
-// forge_mainloop2.h, the gradient stored in fp32 or consumed by the optimizer's epilogue.
+// forge_grouped_wgrad.h -- the optimizer's step of every expert's weight, fused into its gradient
+// dW_e = dY_e^T X_e on the LDS-DMA path of forge_mainloop2.h.  (The gradient kept in fp32 takes the
+// contraction of forge_grouped.h, whose sums are the same bit for bit.)
 //
 // One workgroup of 4 waves takes a 256 x 128 tile of an expert's weight (128 x 128 for the last
 // rows where N is an odd multiple of 128) and contracts the group's rows alone: the operands'
 // buffer ranges begin at the group's first row and end with its last, so a ragged end reads as
-// zero and an empty group contracts nothing.  Two workgroups share a CU: with few rows a group a
-// tile is mostly epilogue (the weight, moments or gradient through memory), and one workgroup's
-// contraction runs beside the other's epilogue.  Experts follow each other in the launch, each
+// zero and an empty group contracts nothing.  Two workgroups share a CU: a tile is mostly epilogue
+// (20 bytes a weight with fp32 moments), and one workgroup's contraction runs beside the other's
+// epilogue; a 256 x 256 tile of one workgroup a CU would have nothing beside it.  8 experts of
+// 4096 x 4096, 8192 rows, AdamW with fp32 moments: 714 us, 3.9 TB/s of the 2.8 GB that it cannot do
+// without (594 us at a copy's 4.75 TB/s) and 385 TFLOP/s besides.  Experts follow each other in the launch, each
 // spread over all XCDs, so that a crowded expert does not hold up one XCD.
 #pragma once
 

@@ -8,8 +8,9 @@
 // registers of one wave (D <= 2048) or of one workgroup of 256 or 512 threads (D <= 16384), 8
 // consecutive elements a thread and vector, so its two sums need no second read; a workgroup
 // walks over rows with the next row's loads in flight while it works on the present one, and
-// keeps its columns' gains (and in the backward pass their gradient's sum) in registers.  Rows
-// that are longer or not 16-byte aligned take the loop kernels at the end of each part.
+// keeps its columns' gains (and in the backward pass their gradient's sum) in registers.  Rows whose
+// bytes are no multiple of 16 (ODD) are loaded by the same vectors, which then straddle lines, their last
+// columns one by one.  Rows that are longer take the loop kernels at the end of each part.
 // Sums and statistics are fp32.
 #include <hip/hip_runtime.h>
 
@@ -65,6 +66,34 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
     st16(static_cast<float*>(p) + i + 4, b);
   }
 }
+// The same from any alignment, and n < 8 elements one by one (the others are 0): rows whose bytes are
+// no multiple of 16.
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
+template <bool BF>
+__device__ __forceinline__ Raw8<BF> load_any(const void* p, int64_t i, int n) {
+  Raw8<BF> r;
+  const int64_t at = i * (BF ? 2 : 4);
+  const char* b = static_cast<const char*>(p) + at;
+  if (n == 8) {
+    r.q[0] = *reinterpret_cast<const u32x4u*>(b);
+    if constexpr (!BF) r.q[1] = *reinterpret_cast<const u32x4u*>(b + 16);
+    return r;
+  }
+  uint32_t v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = j >= n ? 0u : BF ? (uint32_t)reinterpret_cast<const uint16_t*>(b)[j] : reinterpret_cast<const uint32_t*>(b)[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (BF) r.q[0][j] = v[2 * j] | (v[2 * j + 1] << 16);
+    else {
+      r.q[0][j] = v[j];
+      r.q[1][j] = v[4 + j];
+    }
+  }
+  return r;
+}
 template <bool BF>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if constexpr (BF) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
@@ -83,6 +112,41 @@ __device__ __forceinline__ float round_to(float v) {
   if constexpr (BF) return bf16_to_f32(f32_to_bf16_rne(v));
   else return v;
 }
+
+template <bool BF>
+__device__ __forceinline__ void store_any(void* p, int64_t i, const float (&v)[8], int n) {
+  char* b = static_cast<char*>(p) + i * (BF ? 2 : 4);
+  if (n == 8) {
+    u32x4 q[BF ? 1 : 2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF) q[0][j] = f32_to_bf16_rne(v[2 * j]) | (f32_to_bf16_rne(v[2 * j + 1]) << 16);
+      else {
+        q[0][j] = __float_as_uint(v[j]);
+        q[1][j] = __float_as_uint(v[4 + j]);
+      }
+    }
+    *reinterpret_cast<u32x4u*>(b) = q[0];
+    if constexpr (!BF) *reinterpret_cast<u32x4u*>(b + 16) = q[1];
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) store1<BF>(b, j, v[j]);
+}
+
+// A thread's 8 columns of a row, n of them in the row (ODD: the row's bytes are no multiple of 16).
+template <bool BF, bool ODD>
+__device__ __forceinline__ Raw8<BF> load_cols(const void* p, int64_t i, int n) {
+  if constexpr (ODD) return load_any<BF>(p, i, n);
+  else return load8<BF>(p, i);
+}
+template <bool BF, bool ODD>
+__device__ __forceinline__ void store_cols(void* p, int64_t i, const float (&v)[8], int n) {
+  if constexpr (ODD) store_any<BF>(p, i, v, n);
+  else store8<BF>(p, i, v);
+}
+__device__ __forceinline__ int cols_in(int c, int D) { return D - c < 0 ? 0 : D - c > 8 ? 8 : D - c; }
 
 // Clamped to the fp8 range; NaN stays.
 __device__ __forceinline__ float clamp8(float y) { return y > kFp8Max ? kFp8Max : (y < -kFp8Max ? -kFp8Max : y); }
@@ -121,7 +185,7 @@ __device__ __forceinline__ void raise_amax(float* amax, float v) {
 }
 
 // ------------------------------------------------------------------ forward
-template <bool BF, bool RES, int YT, int TPR, int NV>
+template <bool BF, bool RES, bool ODD, int YT, int TPR, int NV>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs a) {
   constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;  // rows at a time
   __shared__ float red[2][2][8];                   // by row parity and use: one barrier a reduction
@@ -129,15 +193,15 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + sub;
   if (row >= a.T) return;  // a whole row's threads; with TPR > 64 a whole workgroup
-  bool in[NV];
+  int in[NV];  // columns of the row in this thread's vector: 0 or 8, or the last few (ODD)
   float gain[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (lane + i * TPR) * 8;
-    in[i] = c < a.D;
+    in[i] = cols_in(c, a.D);
     if (!in[i]) continue;
-    if (a.gain_bf16) unpack8<true>(load8<true>(a.gain, c), gain[i]);
-    else unpack8<false>(load8<false>(a.gain, c), gain[i]);
+    if (a.gain_bf16) unpack8<true>(load_cols<true, ODD>(a.gain, c, in[i]), gain[i]);
+    else unpack8<false>(load_cols<false, ODD>(a.gain, c, in[i]), gain[i]);
   }
   Raw8<BF> x[NV], r[RES ? NV : 1];
   auto fetch = [&](int64_t t) {
@@ -145,8 +209,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       const int64_t at = t * a.D + (lane + i * TPR) * 8;
-      x[i] = load8<BF>(a.x, at);
-      if constexpr (RES) r[i] = load8<BF>(a.res, at);
+      x[i] = load_cols<BF, ODD>(a.x, at, in[i]);
+      if constexpr (RES) r[i] = load_cols<BF, ODD>(a.res, at, in[i]);
     }
   };
   fetch(row);
@@ -163,7 +227,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
         unpack8<BF>(r[i], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = round_to<BF>(v[i][j] + w[j]);
-        store8<BF>(a.h, row * a.D + (lane + i * TPR) * 8, v[i]);
+        store_cols<BF, ODD>(a.h, row * a.D + (lane + i * TPR) * 8, v[i], in[i]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
@@ -179,7 +243,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[i][j] = (v[i][j] * s) * gain[i][j];
-        mx = amax2(mx, fabsf(v[i][j]));
+        if (!ODD || j < in[i]) mx = amax2(mx, fabsf(v[i][j]));
       }
     }
     float inv = 1.0f;
@@ -198,7 +262,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
       if (!in[i]) continue;
       const int64_t at = row * a.D + (lane + i * TPR) * 8;
       if constexpr (YT == FORGE_Y_F32 || YT == FORGE_Y_BF16) {
-        store8<YT == FORGE_Y_BF16>(a.y, at, v[i]);
+        store_cols<YT == FORGE_Y_BF16, ODD>(a.y, at, v[i], in[i]);
       } else {
         u32x2 q;
 #pragma unroll
@@ -208,7 +272,16 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
           w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(v[i][4 * j + 2] * inv), clamp8(v[i][4 * j + 3] * inv), w, true);
           q[j] = (uint32_t)w;
         }
-        st8(static_cast<uint8_t*>(a.y) + at, q);
+        uint8_t* y = static_cast<uint8_t*>(a.y) + at;
+        if constexpr (!ODD) {
+          st8(y, q);
+        } else if (in[i] == 8) {
+          *reinterpret_cast<u32x2u*>(y) = q;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < in[i]) y[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+        }
       }
     }
   }
@@ -219,8 +292,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
   }
 }
 
-// Any D and alignment: one workgroup a row, the row read again for each pass (every thread its
-// own columns).
+// Rows too long for registers: one workgroup a row, the row read again for each pass (every thread
+// its own columns).
 template <bool BF, int YT>
 __global__ __launch_bounds__(256) void rmsnorm_loop_kernel(NormArgs a) {
   __shared__ float red[2][16];
@@ -267,7 +340,7 @@ __global__ __launch_bounds__(256) void rmsnorm_loop_kernel(NormArgs a) {
 // ------------------------------------------------------------------ backward
 // Row group u (TPR threads) takes rows u T / G .. (u + 1) T / G - 1 and writes their share of
 // dgain to row u of the partial sums; dgain_kernel adds the rows in order.
-template <bool BF, bool DH, bool DG, int TPR, int NV>
+template <bool BF, bool DH, bool DG, bool ODD, int TPR, int NV>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(NormBwdArgs a, int64_t groups) {
   constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
   __shared__ float red[2][16];
@@ -277,16 +350,16 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(Norm
   int64_t row = u * a.T / groups;
   const int64_t end = (u + 1) * a.T / groups;
   constexpr bool AHEAD = NV == 1;  // next row's loads in flight, gain in registers
-  bool in[NV];
+  int in[NV];
   float gain[NV][8], acc[DG ? NV : 1][8];
   auto fetch_gain = [&](int i) {
     const int c = (lane + i * TPR) * 8;
-    if (a.gain_bf16) unpack8<true>(load8<true>(a.gain, c), gain[i]);
-    else unpack8<false>(load8<false>(a.gain, c), gain[i]);
+    if (a.gain_bf16) unpack8<true>(load_cols<true, ODD>(a.gain, c, in[i]), gain[i]);
+    else unpack8<false>(load_cols<false, ODD>(a.gain, c, in[i]), gain[i]);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    in[i] = (lane + i * TPR) * 8 < a.D;
+    in[i] = cols_in((lane + i * TPR) * 8, a.D);
     if constexpr (DG)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
@@ -300,9 +373,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(Norm
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
       const int64_t at = t * a.D + (lane + i * TPR) * 8;
-      rdy[i] = load8<BF>(a.dy, at);
-      rh[i] = load8<BF>(a.h, at);
-      if constexpr (DH && AHEAD) rdh[i] = load8<BF>(a.dh, at);
+      rdy[i] = load_cols<BF, ODD>(a.dy, at, in[i]);
+      rh[i] = load_cols<BF, ODD>(a.h, at, in[i]);
+      if constexpr (DH && AHEAD) rdh[i] = load_cols<BF, ODD>(a.dh, at, in[i]);
     }
   };
   if (AHEAD && row < end) fetch(row);
@@ -329,7 +402,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(Norm
       if (!in[i]) continue;
       if (!AHEAD) {
         fetch_gain(i);
-        if constexpr (DH) unpack8<BF>(load8<BF>(a.dh, row * a.D + (lane + i * TPR) * 8), dh[i]);
+        if constexpr (DH) unpack8<BF>(load_cols<BF, ODD>(a.dh, row * a.D + (lane + i * TPR) * 8, in[i]), dh[i]);
       }
       float dx[8];
 #pragma unroll
@@ -338,13 +411,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(Norm
         if constexpr (DH) dx[j] += dh[i][j];
         if constexpr (DG) acc[i][j] = __builtin_fmaf(dy[i][j], h[i][j] * s, acc[i][j]);
       }
-      store8<BF>(a.dx, row * a.D + (lane + i * TPR) * 8, dx);
+      store_cols<BF, ODD>(a.dx, row * a.D + (lane + i * TPR) * 8, dx, in[i]);
     }
   }
   if constexpr (DG)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (in[i]) store8<false>(a.partial, u * a.D + (lane + i * TPR) * 8, acc[i]);
+      if (in[i]) store_cols<false, ODD>(a.partial, u * a.D + (lane + i * TPR) * 8, acc[i], in[i]);
 }
 
 template <bool BF>
@@ -406,7 +479,7 @@ void by_width(int D, F&& f) {
   else if (D <= 8192) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
   else f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
 }
-bool in_registers(int D) { return D % 8 == 0 && D <= 16384; }
+bool in_registers(int D) { return D <= 16384; }
 
 template <bool BF, int YT>
 void forward(const NormArgs& a, hipStream_t st) {
@@ -419,8 +492,9 @@ void forward(const NormArgs& a, hipStream_t st) {
     constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR, THREADS = TPR > 256 ? TPR : 256;
     const int64_t blocks = (a.T + RPB - 1) / RPB;
     const unsigned grid = (unsigned)(blocks < kNormBlocks ? blocks : kNormBlocks);
-    if (a.res) hipLaunchKernelGGL((rmsnorm_kernel<BF, true, YT, TPR, NV>), dim3(grid), dim3(THREADS), 0, st, a);
-    else hipLaunchKernelGGL((rmsnorm_kernel<BF, false, YT, TPR, NV>), dim3(grid), dim3(THREADS), 0, st, a);
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(THREADS), 0, st, a); };
+    if (a.D % 8) launch(a.res ? rmsnorm_kernel<BF, true, true, YT, TPR, NV> : rmsnorm_kernel<BF, false, true, YT, TPR, NV>);
+    else launch(a.res ? rmsnorm_kernel<BF, true, false, YT, TPR, NV> : rmsnorm_kernel<BF, false, false, YT, TPR, NV>);
   });
 }
 
@@ -442,8 +516,8 @@ void backward(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
   by_width_backward(a.D, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR, THREADS = TPR > 256 ? TPR : 256;
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF, DH, DG, TPR, NV>), dim3((unsigned)((groups + RPB - 1) / RPB)),
-                       dim3(THREADS), 0, st, a, groups);
+    hipLaunchKernelGGL((a.D % 8 ? rmsnorm_bwd_kernel<BF, DH, DG, true, TPR, NV> : rmsnorm_bwd_kernel<BF, DH, DG, false, TPR, NV>),
+                       dim3((unsigned)((groups + RPB - 1) / RPB)), dim3(THREADS), 0, st, a, groups);
   });
 }
 

@@ -563,3 +563,13 @@ def test_grouped_products_repeat_bit_for_bit(lib):
             lib.grouped_gemm(X, W, ends, Y)
     s.synchronize()
     assert torch.equal(Y, first)
+
+
+# ------------------------------------------------------------------ norms of rows that are not 16-byte aligned
+@pytest.mark.parametrize("D", [9, 513, 1023, 1025, 2047, 4099, 5121, 6149, 8191, 8193, 16383, 16385])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_norm_odd_widths(lib, D, dt):
+    """One width at least in every class of row kernels, and the ends of the classes."""
+    for res in (True, False):
+        test_norm_forward(lib, D, dt, res)
+        test_norm_backward(lib, D, dt, res)
