@@ -53,12 +53,13 @@ __device__ __forceinline__ void wgrad_tile_f32(const GroupedWgradArgs& a, float*
 
 __global__ __launch_bounds__(THREADS, 1) void grouped_wgrad_kernel(GroupedWgradArgs a, float* dW) {
   __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * 32768];
-  const int nbn = (int)((a.N + 255) / 256), nbk = (int)((a.K + 255) / 256), per = nbn * nbk;
+  const int side = a.small ? 128 : 256;
+  const int nbn = (int)((a.N + side - 1) / side), nbk = (int)((a.K + side - 1) / side), per = nbn * nbk;
   const int e = (int)blockIdx.x / per, b = (int)blockIdx.x - e * per;
   int start, len;
   group_rows(a.ends, a.E, a.T, e, start, len);
-  const int n0 = 256 * (b % nbn), k0 = 256 * (b / nbn);
-  const bool low = a.N - n0 < 256, narrow = a.K - k0 < 256;
+  const int n0 = side * (b % nbn), k0 = side * (b / nbn);
+  const bool low = a.small || a.N - n0 < 256, narrow = a.small || a.K - k0 < 256;
   if (!low && !narrow) wgrad_tile_f32<4, 4>(a, dW, e, start, len, n0, k0, smem);
   else if (!narrow) wgrad_tile_f32<2, 4>(a, dW, e, start, len, n0, k0, smem);
   else if (!low) wgrad_tile_f32<4, 2>(a, dW, e, start, len, n0, k0, smem);
@@ -67,18 +68,24 @@ __global__ __launch_bounds__(THREADS, 1) void grouped_wgrad_kernel(GroupedWgradA
 
 }  // namespace grp
 
-int launch_grouped_wgrad(const GroupedWgradArgs& a, float* dW, void* stream) {
-  const dim3 grid((unsigned)(a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256)));
+int launch_grouped_wgrad(const GroupedWgradArgs& given, float* dW, void* stream) {
+  GroupedWgradArgs a = given;
+  int64_t tiles = ((a.N + 255) / 256) * ((a.K + 255) / 256);
+  a.small = grp::wgrad_small(a.E, tiles);
+  if (a.small) tiles = (a.N / 128) * (a.K / 128);
+  const dim3 grid((unsigned)(a.E * tiles));
   hipLaunchKernelGGL(grp::grouped_wgrad_kernel, grid, dim3(grp::THREADS), 0, (hipStream_t)stream, a, dW);
   return (int)hipGetLastError();
 }
 
-int launch_grouped_step(int s_type, int opt, const GroupedWgradArgs& a, const EpiArgs& e, void* stream) {
+int launch_grouped_step(int s_type, int opt, const GroupedWgradArgs& given, const EpiArgs& e, void* stream) {
+  GroupedWgradArgs a = given;
+  a.small = grp::wgrad_small(a.E, grp::wgrad_tiles(a.N, a.K, false));
   grp::GroupedStepFn fn = s_type == FORGE_S_F32  ? grp::select_grouped_step<FORGE_S_F32>(opt)
                           : s_type == FORGE_S_Q8 ? grp::select_grouped_step<FORGE_S_Q8>(opt)
                                                  : grp::select_grouped_step<FORGE_S_Q8D>(opt);
   if (!fn) return (int)hipErrorInvalidValue;
-  const dim3 grid((unsigned)(a.E * (int64_t)grp::wgrad_tiles(a.N, a.K)));
+  const dim3 grid((unsigned)(a.E * (int64_t)grp::wgrad_tiles(a.N, a.K, a.small)));
   hipLaunchKernelGGL(fn, grid, dim3(ml2::THREADS), 0, (hipStream_t)stream, a, e);
   return (int)hipGetLastError();
 }

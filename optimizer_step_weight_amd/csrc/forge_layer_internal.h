@@ -66,6 +66,7 @@ struct GroupedWgradArgs {
   const void* dY;
   const int32_t* ends;
   int32_t E;
+  int32_t small;         // 128 x 128 tiles throughout
   int64_t T, N, K;
 };
 int launch_grouped_wgrad(const GroupedWgradArgs& a, float* dW, void* stream);

@@ -573,3 +573,24 @@ def test_norm_odd_widths(lib, D, dt):
     for res in (True, False):
         test_norm_forward(lib, D, dt, res)
         test_norm_backward(lib, D, dt, res)
+
+
+@pytest.mark.parametrize("E,N,K", [(3, 384, 512), (40, 384, 512), (40, 512, 640)])
+def test_grouped_gradient_and_step_on_small_and_large_tiles(lib, E, N, K):
+    """Few tiles (all 128 x 128) and many (the larger ones, and 128 rows or columns left over)."""
+    g = gen(E + N)
+    rows = torch.randint(0, 90, (E,), generator=g)
+    rows[0] = 300
+    ends = [int(x) for x in rows.cumsum(0)]
+    T = ends[-1]
+    X, dY = ints((T, K), 4, 31), ints((T, N), 4, 32)
+    Xd, Dd, ed = X.cuda(), dY.cuda(), torch.tensor(ends, dtype=torch.int32, device="cuda")
+    dW = torch.full((E, N, K), float("nan"), device="cuda")
+    lib.grouped_wgrad(Xd, Dd, ed, dW)
+    assert torch.equal(dW.cpu(), R.grouped_wgrad(X, dY, ends).float())
+    W = (0.05 * torch.randn(E, N, K, generator=g)).to(BF).cuda()
+    a, b = ([W.clone(), torch.zeros(E, N, K, device="cuda"), torch.zeros(E, N, K, device="cuda")] for _ in range(2))
+    kw = dict(opt="adamw", hyper=HYPER, step=2, seed=3)
+    lib.grouped_wgrad_step(Xd, Dd, ed, *a, **kw)
+    lib.optimizer_step(dW.view(E * N, K), *(t.view(E * N, K) for t in b), **kw)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
