@@ -345,8 +345,8 @@ struct Tile {
     }
   }
 
-  // Before and after the matrix instructions that the compiler does not see: every register written
-  // before is there (19 wait states at most, after a 32 x 32 x 64 product).
+  // After the matrix instructions that the compiler does not see: their last results are written
+  // (19 wait states at most, after a 32 x 32 x 64 product).
   static __device__ __forceinline__ void settle() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
@@ -395,6 +395,9 @@ struct Tile {
     constexpr int H = MB * NB;
     constexpr int FREE = 10 * H / 16, LANDED = 22 * H / 16, G_END = 7 * H / 16, F_END = 29 * H / 16;
     constexpr int A_FROM = 26 * H / 16;
+    // two wait states from a vector instruction that writes an accumulator (the zeroes before the first
+    // slab) to a matrix instruction that reads it
+    asm volatile("s_nop 1" ::: "memory");
     static_for<2 * H>([&](auto nc) {
       constexpr int n = decltype(nc)::value;
       // the scalar work, a few instructions at a time
@@ -472,7 +475,6 @@ struct Tile {
     Frags f, g;
     static_for<READS>([&](auto n) { read<0, n>(f, to_a, to_b); });
     Places at{to_a, 0, to_a + 2 * A::PANEL, to_a, to_a + STAGES_A * A::PANEL, to_b, 0, 2 * to_b + B::PANEL};
-    settle();  // the zeroes are written
     for (int s = slabs; s > 0; --s) step(f, g, fa, fb, at);
     settle();
     wait_vm<0>();  // no copy may land after the workgroup's end
@@ -523,6 +525,11 @@ struct Tile {
   }
 };
 
+// A store that is not kept in L2 in favour of the operands.
+__device__ __forceinline__ void st16_stream(void* p, u32x4 q) {
+  __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
+}
+
 // Two values to bf16, nearest even, in one instruction.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -571,7 +578,7 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, const RowTile& t
         return u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
       },
       [&](int row, int col, u32x4 q) {
-        if (row < rows) st16(out + (int64_t)row * O + col, q);
+        if (row < rows) st16_stream(out + (int64_t)row * O + col, q);
       });
 }
 

