@@ -13,9 +13,10 @@
 // PFLOP/s); in even groups 1.36 ms, where eight calls of the library, one an expert, take 1.42 and
 // its product of one weight of that size 1.26.  16384 rows of 32 experts by 4096 x 4096 in fp8
 // 0.30-0.31 ms (1.8 PFLOP/s).  Input gradient of 32768 rows of 64 experts by 1408 x 2048 0.21 ms.
-// The card's power bounds the long ones: the clock falls to 1.6-1.7 GHz while the matrix cores are
-// 85 % busy within a tile.  The rest is what a workgroup alone on its CU cannot hide: 2.4 thousand cycles to
-// find its tile, 5 until its first slabs have come, 7 to store, beside 2.3 a slab.
+// The card's power bounds the bf16 product: the clock falls to 1.6-1.7 GHz while the matrix cores are
+// 85 % busy within a tile (74 % over the launch).  The others are at 41 % and 42 % and 2 GHz: shorter
+// contractions over more, ragged groups.  There it is what a workgroup alone on its CU cannot hide:
+// 2.4 thousand cycles to find its tile, 5 until its first slabs have come, 7 to store, beside 2.3 a slab.
 #pragma once
 
 #include "forge_layer_internal.h"
