@@ -577,7 +577,7 @@ __device__ __forceinline__ void rows_tile(const GroupedArgs& a, const RowTile& t
             const float sa = row < rows ? as[row] : 0.0f;
             const floatx4u sw = *reinterpret_cast<const floatx4u*>(ws + col);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) v[x] *= sa * sw[x];
+            for (int x = 0; x < 4; ++x) v[x] = (v[x] * sa) * sw[x];  // the scales' product may leave fp32's range
           }
         }
         return u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};

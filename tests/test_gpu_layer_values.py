@@ -92,3 +92,18 @@ def test_fp8_product_repeats_and_nan_stays(lib):
     bad = torch.zeros(T, N, dtype=torch.bool, device="cuda")
     bad[7], bad[ends[1]:ends[2], 300] = True, True
     assert torch.isnan(Y[bad]).all() and torch.equal(Y[~bad], first[~bad])
+
+
+def test_fp8_product_of_scales_whose_product_leaves_fp32(lib):
+    """x_scale w_scale is not representable, the result is: the sum takes the scales one after the other."""
+    T, N, K = 70, 256, 1024
+    X, W = torch.full((T, K), 448.0).to(FP8), torch.full((1, N, K), 448.0).to(FP8)
+    X[1], W[0, 3] = 0, 0
+    xs, ws = torch.full((T,), 2.0 ** -90), torch.full((1, N), 2.0 ** -60)
+    xs[1], ws[0, 3], xs[0], ws[0, 5] = 2.0 ** 100, 2.0 ** 100, 2.0 ** 100, 2.0 ** -120
+    Y = torch.empty(T, N, dtype=BF, device="cuda")
+    lib.grouped_gemm(X.cuda(), W.cuda(), torch.tensor([T], dtype=torch.int32, device="cuda"), Y, x_scale=xs.cuda(),
+                     w_scale=ws.cuda())
+    s = xs.to(R.F64)[:, None] * ws[0].to(R.F64)[None]
+    want = (X.to(R.F64) @ W[0].to(R.F64).t()) * s
+    near(Y, want, (HALF[BF] + 4 * R.U) * want.abs() + 2.0 ** -134)   # equal products: the sum is exact
