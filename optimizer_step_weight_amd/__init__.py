@@ -177,6 +177,17 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _workspace(count: int, dtype, device, stream):
+    """A buffer for one call that runs on `stream` (None: the current one), allocated as that
+    stream's memory: the allocator hands it to other work of that stream alone, in order, from
+    the moment that the last reference is dropped."""
+    import torch
+    if stream is None:
+        return torch.empty(count, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device)):
+        return torch.empty(count, dtype=dtype, device=device)
+
+
 def _opts(w_preround_out, sr, W):
     if w_preround_out is None and sr:
         return None

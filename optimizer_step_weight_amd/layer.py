@@ -13,7 +13,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import (BF16, F32, FP8_E4M3, I8_B64, I8DYN_B64, U8_B64, U8DYN_B64, Hyper, StepOpts, Tensor, _check, _dyn,
-               _hyper, _lib, _opt, _opts, _ref, _stream, _tensor)
+               _hyper, _lib, _opt, _opts, _ref, _stream, _tensor, _workspace)
 
 SCALE_MODE = {"row": 0, "tensor": 1}
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
@@ -133,23 +133,24 @@ def rmsnorm(x, gain, y, *, residual=None, h=None, rstd=None, y_scale=None, amax=
         None if amax is None else _vec(amax, "amax", 1, dev), _stream(stream, dev)))
 
 
-def rmsnorm_backward_workspace(rows: int, width: int, device="cuda") -> torch.Tensor:
-    """A workspace for rmsnorm_backward of [rows, width] tensors."""
+def rmsnorm_backward_workspace(rows: int, width: int, device="cuda", *, stream=None) -> torch.Tensor:
+    """A workspace for rmsnorm_backward of [rows, width] tensors, allocated for work on `stream`
+    (default: the current stream)."""
     n = _lib().forge_rmsnorm_backward_workspace_bytes(int(rows), int(width))
     if n < 0:
         raise ValueError(f"no workspace for [{rows}, {width}]")
-    return torch.empty(n // 4, dtype=torch.float32, device=device)
+    return _workspace(n // 4, torch.float32, device, stream)
 
 
 def rmsnorm_backward(dy, h, gain, rstd, dx, dgain=None, *, dh=None, workspace=None, stream=None) -> None:
     """dx (of x and of residual; dh, the gradient arriving on h itself, is added) and dgain
-    (float32, overwritten) of rmsnorm (forge_rmsnorm_backward).  A workspace is allocated where
-    dgain is wanted and none is given."""
+    (float32, overwritten) of rmsnorm (forge_rmsnorm_backward).  A workspace is allocated, for the
+    stream of the call, where dgain is wanted and none is given."""
     dev = _device(h, "h")
     H = _mat(h, "h", dev)
     rows, width = H.rows, H.cols
     if dgain is not None and workspace is None:
-        workspace = rmsnorm_backward_workspace(rows, width, h.device)
+        workspace = rmsnorm_backward_workspace(rows, width, h.device, stream=stream)
     if workspace is not None:
         _here(workspace, "workspace", dev)
         if not workspace.is_contiguous():

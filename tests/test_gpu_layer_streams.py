@@ -1,0 +1,52 @@
+"""Buffers that the binding owns, when the work runs on another stream than the current one: they are not
+handed to other work before that stream is done with them."""
+import pytest
+import torch
+
+from tests import layer_ref as R
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+BUSY = 50_000_000      # clock ticks that keep a stream busy: some tens of milliseconds
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import optimizer_step_weight_amd as forge
+    forge.device_check(0)
+    return forge
+
+
+@pytest.fixture(autouse=True)
+def _name(request):
+    print("[case]", request.node.name, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def fill_new_blocks(size, count=4):
+    """New blocks of `size` bytes on the current stream, written at once."""
+    return [torch.full((size // 4,), float("nan"), device="cuda") for _ in range(count)]
+
+
+def test_norm_backward_workspace_belongs_to_the_stream(lib):
+    T, D = 700, 1024
+    g = torch.Generator().manual_seed(1)
+    h, dy, gain = torch.randn(T, D, generator=g).to(BF), torch.randn(T, D, generator=g).to(BF), torch.ones(D)
+    rstd = R.norm(h, gain, 1e-6)[1].float()
+    h, dy, gain, rstd = (t.cuda() for t in (h, dy, gain, rstd))
+    size = 4 * lib.rmsnorm_backward_workspace(T, D).numel()
+    dx, dgain, dx1, dgain1 = torch.empty_like(h), torch.empty(D, device="cuda"), torch.empty_like(h), torch.empty(D, device="cuda")
+    lib.rmsnorm_backward(dy, h, gain, rstd, dx, dgain)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    lib.rmsnorm_backward(dy, h, gain, rstd, dx1, dgain1, stream=s.cuda_stream)
+    kept = fill_new_blocks(size)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx1) and torch.equal(dgain, dgain1)
+    assert all(torch.isnan(t).all() for t in kept)
+    # the default stream by its address
+    lib.rmsnorm_backward(dy, h, gain, rstd, dx1.zero_(), dgain1.zero_(), stream=0)
+    assert torch.equal(dx, dx1) and torch.equal(dgain, dgain1)
