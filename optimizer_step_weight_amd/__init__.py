@@ -245,13 +245,13 @@ def linear_backward_step_fused(X, dY, W, dX, m=None, v=None, *, opt="adamw", hyp
                                m_scale=None, v_scale=None, w_preround_out=None, sr=True, state_map="linear",
                                workspace=None, stream=None):
     """dgrad and the fused step in one launch (forge_linear_backward_step_fused).  `workspace` is a
-    device tensor of at least backward_workspace_bytes(K) bytes; one is allocated when it is None.
+    device tensor of at least backward_workspace_bytes(K) bytes; one is allocated, as memory of the
+    call's stream, when it is None.
     Returns the workspace (its int32 word 1 is nonzero if a wait hit its bound)."""
-    import torch
     o = _opts(w_preround_out, sr, W)
     dyn = _dyn(state_map)
     if workspace is None:
-        workspace = torch.empty(backward_workspace_bytes(W.shape[1]) // 4, dtype=torch.int32, device=W.device)
+        workspace = _workspace(backward_workspace_bytes(W.shape[1]) // 4, torch.int32, W.device, stream)
     _on_device(workspace, "workspace")
     _check(_lib().forge_linear_backward_step_fused(
         _ref(_tensor(X)), _ref(_tensor(dY)), _ref(_tensor(W)), _ref(_tensor(dX)), _ref(_tensor(m, m_scale, dyn)),

@@ -50,3 +50,24 @@ def test_norm_backward_workspace_belongs_to_the_stream(lib):
     # the default stream by its address
     lib.rmsnorm_backward(dy, h, gain, rstd, dx1.zero_(), dgain1.zero_(), stream=0)
     assert torch.equal(dx, dx1) and torch.equal(dgain, dgain1)
+
+
+def test_one_launch_backward_workspace_belongs_to_the_stream(lib):
+    T, N, K = 256, 256, 384
+    g = torch.Generator().manual_seed(2)
+    X, dY = torch.randn(T, K, generator=g).to(BF).cuda(), (0.1 * torch.randn(T, N, generator=g)).to(BF).cuda()
+    W0 = (0.05 * torch.randn(N, K, generator=g)).to(BF).cuda()
+    size = lib.backward_workspace_bytes(K)
+    s, out = torch.cuda.Stream(), []
+    for stream in (None, s.cuda_stream, 0):
+        W, m, v, dX = W0.clone(), torch.zeros(N, K, device="cuda"), torch.zeros(N, K, device="cuda"), torch.empty_like(X)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(BUSY)
+        lib.linear_backward_step_fused(X, dY, W, dX, m, v, step=1, seed=3, stream=stream)   # the workspace is dropped
+        kept = fill_new_blocks(size)
+        torch.cuda.synchronize()
+        out.append((W, m, v, dX))
+        assert all(torch.isnan(t).all() for t in kept)
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))
