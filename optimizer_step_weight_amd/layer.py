@@ -235,27 +235,27 @@ class MultiStep:
                  state_map: str = "linear"):
         self.opt, self._dyn = _opt(opt), _dyn(state_map)
         n = len(W)
-        self._lists = {"W": list(W)}
+        lists = {"W": list(W)}
         for name, x in (("g", g), ("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale)):
             if x is not None and len(x) != n:
                 raise ValueError(f"{name} has {len(x)} tensors, W has {n}")
-            self._lists[name] = None if x is None else list(x)
+            lists[name] = None if x is None else list(x)
         self.group = [0] * n if group is None else [int(x) for x in group]
         self.seed = list(range(n)) if seed is None else [int(x) & 0xFFFFFFFFFFFFFFFF for x in seed]
         if len(self.group) != n or len(self.seed) != n:
             raise ValueError("group and seed take one entry for each tensor")
-        self._device = None
-        self._pack()
+        self._hypers, self._given = (Hyper * 8)(), None
+        self._pack(lists)
 
     def set_grads(self, g: Sequence) -> None:
-        """Takes other gradient tensors (the table is packed and copied anew)."""
+        """Takes other gradient tensors (the table is packed and copied anew).  Where they are refused,
+        the plan keeps those that it had."""
         if len(g) != len(self._lists["W"]):
             raise ValueError(f"g has {len(g)} tensors, W has {len(self._lists['W'])}")
-        self._lists["g"] = list(g)
-        self._pack()
+        self._pack(dict(self._lists, g=list(g)))
 
-    def _pack(self) -> None:
-        L = self._lists
+    def _pack(self, L: dict) -> None:
+        """Checks and packs the tensors; the plan takes them all at once, at the end."""
         n = len(L["W"])
         if L["g"] is None:
             raise ValueError("g is None")
@@ -289,13 +289,12 @@ class MultiStep:
         lib = _lib()
         size = lib.forge_multi_table_bytes(entries, n)
         host = torch.empty(max(size, 16), dtype=torch.uint8)
-        self._info = _MultiInfo()
+        info = _MultiInfo()
         _check(lib.forge_multi_pack(entries, n, self.opt, codes["m"], codes["v"], host.data_ptr(), host.numel(),
-                                    ctypes.byref(self._info)))
-        self._hypers, self._given = (Hyper * 8)(), None
-        if n:
-            self._device = dev
-            self._table = host.to(L["W"][0].device)   # a synchronous copy: the table is there for any stream
+                                    ctypes.byref(info)))
+        # a synchronous copy: the table is there for any stream
+        table = host.to(L["W"][0].device) if n else None
+        self._lists, self._info, self._table, self._device = L, info, table, dev if n else None
 
     def step(self, *, step: int, hyper=None, grad_scale: Optional[torch.Tensor] = None, sr: bool = True,
              stream=None) -> None:

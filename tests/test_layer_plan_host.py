@@ -1,0 +1,64 @@
+"""MultiStep's host side, no GPU needed: the plan packs host tensors here (their addresses are never used),
+so that its table, its state after a refusal and its hyper-parameters can be looked at."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+
+@pytest.fixture()
+def f(monkeypatch):
+    import optimizer_step_weight_amd as forge
+    if not os.path.exists(forge.LIB_PATH):
+        from optimizer_step_weight_amd import _build
+        _build.build(verbose=False)
+    from optimizer_step_weight_amd import layer
+    monkeypatch.setattr(layer, "_device", lambda t, what: -1)     # where a host tensor says it is
+    monkeypatch.setattr(layer, "_current_device", lambda: -1)
+    return forge
+
+
+def plan_of(f, sizes=(5, 4096, 70_000)):
+    W, g, m, v = ([torch.zeros(n) for n in sizes] for _ in range(4))
+    return f.MultiStep(W, g, m, v, opt="adamw"), W, g
+
+
+def state(plan):
+    info = plan._info
+    return bytes(ctypes.string_at(ctypes.addressof(info), ctypes.sizeof(info))), plan._table.clone(), plan._lists["g"]
+
+
+@pytest.mark.parametrize("bad", ["type", "size", "count", "alias", "alignment", "none"])
+def test_refused_gradients_leave_the_plan_as_it_was(f, bad):
+    plan, W, g = plan_of(f)
+    info, table, grads = state(plan)
+    new = [torch.ones_like(t) for t in g]
+    if bad == "type":
+        new[2] = new[2].to(torch.float16)
+    elif bad == "size":
+        new[1] = new[1][:-1]
+    elif bad == "count":
+        new = new[:2]
+    elif bad == "alias":
+        new[2] = W[2]
+    elif bad == "alignment":
+        new[1] = torch.ones(4097)[1:]
+    else:
+        new[0] = None
+    with pytest.raises((ValueError, TypeError, AttributeError, f.ForgeError)):
+        plan.set_grads(new)
+    after = state(plan)
+    assert after[0] == info and torch.equal(after[1], table)
+    assert len(after[2]) == len(grads) and all(a is b for a, b in zip(after[2], grads))
+
+
+def test_gradients_taken(f):
+    plan, _, g = plan_of(f)
+    _, table, _ = state(plan)
+    new = [torch.ones_like(t) for t in g]
+    plan.set_grads(new)
+    info, other, grads = state(plan)
+    assert not torch.equal(table, other) and all(a is b for a, b in zip(grads, new))
+    at = [int.from_bytes(bytes(other[72 * i + 8:72 * i + 16].tolist()), "little") for i in range(3)]
+    assert at == [t.data_ptr() for t in new]
