@@ -304,9 +304,12 @@ class MultiStep:
         if len(hypers) > 8:
             raise ValueError("at most 8 groups of hyper-parameters")
         if self._given is None or self._given != hypers:   # by value: they seldom change from step to step
-            for i, h in enumerate(hypers):
-                self._hypers[i] = _hyper(h)
-            self._given = [dict(h) for h in hypers] if all(isinstance(h, dict) for h in hypers) else None
+            taken = [_hyper(h) for h in hypers]            # all of them, or none where one is refused
+            for i, h in enumerate(taken):
+                self._hypers[i] = h
+            # comparable by value only where nothing in them can be changed in place
+            plain = all(isinstance(h, dict) and all(isinstance(x, (float, int)) for x in h.values()) for h in hypers)
+            self._given = [dict(h) for h in hypers] if plain else None
         dev = self._device
         table = None
         if dev is not None:

@@ -62,3 +62,54 @@ def test_gradients_taken(f):
     assert not torch.equal(table, other) and all(a is b for a, b in zip(grads, new))
     at = [int.from_bytes(bytes(other[72 * i + 8:72 * i + 16].tolist()), "little") for i in range(3)]
     assert at == [t.data_ptr() for t in new]
+
+
+def steps(f, plan, monkeypatch):
+    """Calls of step() with the device's call replaced: the learning rates that it would be given."""
+    from optimizer_step_weight_amd import layer
+    seen = []
+
+    class Lib:
+        @staticmethod
+        def forge_multi_step(info, table, hypers, n, *rest):
+            seen.append([round(hypers[i].lr, 6) for i in range(n)])
+            return 0
+    monkeypatch.setattr(layer, "_lib", lambda: Lib)
+    monkeypatch.setattr(layer, "_stream", lambda stream, dev: 0)
+
+    def call(hyper):
+        plan.step(step=1, hyper=hyper)
+        return seen[-1]
+    return call
+
+
+def test_hyper_parameters_of_a_failed_call_are_not_used(f, monkeypatch):
+    plan, _, _ = plan_of(f)
+    call = steps(f, plan, monkeypatch)
+    a, b = {"lr": 1.0}, {"lr": 2.0}
+    assert call([a, b]) == [1.0, 2.0]
+    with pytest.raises(TypeError):
+        call([{"lr": 9.0}, {"lr": "fast"}])
+    assert call([a, b]) == [1.0, 2.0]
+    assert call([b, a]) == [2.0, 1.0] and call(a) == [1.0] and call([a, b]) == [1.0, 2.0]
+
+
+@pytest.mark.parametrize("kind", ["tensor", "array", "object"])
+def test_hyper_parameters_changed_in_place_are_read_again(f, monkeypatch, kind):
+    import types
+
+    import numpy as np
+    plan, _, _ = plan_of(f)
+    call = steps(f, plan, monkeypatch)
+    lr = torch.tensor(1.0) if kind == "tensor" else np.array(1.0)
+    h = types.SimpleNamespace(lr=1.0) if kind == "object" else {"lr": lr}
+    assert call(h) == [1.0]
+    if kind == "object":
+        h.lr = 3.0
+    else:
+        lr[...] = 3.0
+    assert call(h) == [3.0]
+    d = {"lr": 0.5}
+    assert call(d) == [0.5]
+    d["lr"] = 0.25
+    assert call(d) == [0.25]
