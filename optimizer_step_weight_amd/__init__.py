@@ -248,6 +248,7 @@ def linear_backward_step_fused(X, dY, W, dX, m=None, v=None, *, opt="adamw", hyp
     device tensor of at least backward_workspace_bytes(K) bytes; one is allocated, as memory of the
     call's stream, when it is None.
     Returns the workspace (its int32 word 1 is nonzero if a wait hit its bound)."""
+    import torch
     o = _opts(w_preround_out, sr, W)
     dyn = _dyn(state_map)
     if workspace is None:
