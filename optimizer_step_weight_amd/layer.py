@@ -62,6 +62,7 @@ def _declare(L) -> None:
 _byref = ctypes.byref
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _here(t: torch.Tensor, what: str, dev: int) -> None:
@@ -226,7 +227,10 @@ class MultiStep:
     (default: all the first).  seed: stochastic-rounding key of each tensor (default: its index).
 
     The plan holds its tensors and their addresses: gradients are to be written into the same
-    tensors before every step (or set_grads() called with others).
+    tensors before every step (or set_grads() called with others).  set_grads() and dropping the plan
+    leave steps that are still queued on any stream as they are; that stream has to live as long as
+    the plan.  A graph that captured a step goes on with the tensors of that time: it needs the plan,
+    and is to be captured anew where it shall take other gradients.
     """
 
     def __init__(self, W: Sequence, g: Sequence, m: Optional[Sequence] = None, v: Optional[Sequence] = None, *,
@@ -245,6 +249,7 @@ class MultiStep:
         if len(self.group) != n or len(self.seed) != n:
             raise ValueError("group and seed take one entry for each tensor")
         self._hypers, self._given = (Hyper * 8)(), None
+        self._captured = []
         self._pack(lists)
 
     def set_grads(self, g: Sequence) -> None:
@@ -295,6 +300,22 @@ class MultiStep:
         # a synchronous copy: the table is there for any stream
         table = host.to(L["W"][0].device) if n else None
         self._lists, self._info, self._table, self._device = L, info, table, dev if n else None
+        self._home = _stream(None, dev) if n else None   # the allocator orders the table's reuse after this one
+        self._held = set()
+
+    def _hold(self, stream: int) -> None:
+        """Keeps the table and the tensors from reuse until the steps on `stream`, which is not (known to be) the
+        one that the table was allocated on, are done: for good where the stream is captured into a graph."""
+        s = torch.cuda.ExternalStream(stream, device=self._device)
+        with torch.cuda.stream(s):
+            captured = _capturing()
+        if captured:
+            if not self._captured or self._captured[-1][0] is not self._table:
+                self._captured.append((self._table, self._lists))
+        elif stream not in self._held:   # once: the allocator remembers it
+            for t in [self._table, *(t for x in self._lists.values() if x is not None for t in x)]:
+                t.record_stream(s)
+            self._held.add(stream)
 
     def step(self, *, step: int, hyper=None, grad_scale: Optional[torch.Tensor] = None, sr: bool = True,
              stream=None) -> None:
@@ -316,10 +337,13 @@ class MultiStep:
             if dev != _current_device():
                 raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
             table = self._table.data_ptr()
+            launch = _stream(stream, dev)
+            if stream is not None or launch != self._home or _capturing():
+                self._hold(launch)
         _check(_lib().forge_multi_step(
             _byref(self._info), table, self._hypers, len(hypers), int(step),
             None if grad_scale is None else _vec(grad_scale, "grad_scale", 1, dev),
-            None if sr else _NO_SR, None if dev is None else _stream(stream, dev)))
+            None if sr else _NO_SR, None if dev is None else launch))
 
 
 # the C ABI names

@@ -71,3 +71,65 @@ def test_one_launch_backward_workspace_belongs_to_the_stream(lib):
         assert all(torch.isnan(t).all() for t in kept)
     for other in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(out[0], other))
+
+
+def busy_step(lib, s):
+    """A plan and its tensors, with a step queued on s behind other work."""
+    w, g = [torch.zeros(300, device="cuda"), torch.zeros(5000, device="cuda")], None
+    g = [torch.ones_like(t) for t in w]
+    plan = lib.MultiStep(w, g, opt="sgd")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    plan.step(step=1, hyper={"lr": 1.0}, stream=s.cuda_stream)
+    return plan, w, g
+
+
+def test_table_outlives_a_step_on_another_stream(lib):
+    """Both after set_grads and after the plan is gone, also where the step's stream is the current one."""
+    s = torch.cuda.Stream()
+    plan, w, g = busy_step(lib, s)
+    size = plan._table.numel()
+    plan.set_grads([torch.full_like(t, 2.0) for t in w])
+    kept = fill_new_blocks(size)
+    torch.cuda.synchronize()
+    assert all(bool((t == -1.0).all()) for t in w)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+        plan.step(step=2, hyper={"lr": 1.0})
+    del plan
+    kept += fill_new_blocks(size)
+    torch.cuda.synchronize()
+    assert all(bool((t == -3.0).all()) for t in w)
+    plan, w, g = busy_step(lib, s)
+    del plan
+    kept += fill_new_blocks(size)
+    torch.cuda.synchronize()
+    assert all(bool((t == -1.0).all()) for t in w) and all(torch.isnan(t).all() for t in kept)
+
+
+@pytest.mark.parametrize("home", [False, True])
+def test_captured_step_keeps_its_table_and_gradients(lib, home):
+    """A graph replays with the gradients of its capture, whatever set_grads did since."""
+    s = torch.cuda.Stream()
+    w, graph = [torch.zeros(300, device="cuda"), torch.zeros(5000, device="cuda")], torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s) if home else torch.cuda.stream(torch.cuda.current_stream()):
+        plan = lib.MultiStep(w, [torch.ones_like(t) for t in w], opt="sgd")
+        size = plan._table.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        plan.step(step=1, hyper={"lr": 1.0})
+        plan.step(step=1, hyper={"lr": 1.0})
+    total = 0.0
+    for i in range(3):
+        with torch.cuda.stream(s):
+            plan.set_grads([torch.full_like(t, 4.0) for t in w])
+            kept = fill_new_blocks(size) + [torch.full_like(t, float("nan")) for t in w]
+        torch.cuda.synchronize()
+        graph.replay()
+        plan.step(step=2, hyper={"lr": 1.0})
+        torch.cuda.synchronize()
+        total += 2.0 + 4.0
+        assert all(bool((t == -total).all()) for t in w) and all(torch.isnan(t).all() for t in kept)
+    assert len(plan._captured) == 1

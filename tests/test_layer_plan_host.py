@@ -16,6 +16,8 @@ def f(monkeypatch):
     from optimizer_step_weight_amd import layer
     monkeypatch.setattr(layer, "_device", lambda t, what: -1)     # where a host tensor says it is
     monkeypatch.setattr(layer, "_current_device", lambda: -1)
+    monkeypatch.setattr(layer, "_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(layer, "_capturing", lambda: False)
     return forge
 
 
@@ -75,7 +77,6 @@ def steps(f, plan, monkeypatch):
             seen.append([round(hypers[i].lr, 6) for i in range(n)])
             return 0
     monkeypatch.setattr(layer, "_lib", lambda: Lib)
-    monkeypatch.setattr(layer, "_stream", lambda stream, dev: 0)
 
     def call(hyper):
         plan.step(step=1, hyper=hyper)
