@@ -196,16 +196,36 @@ class _RMSNorm(torch.autograd.Function):
         h, gain, rstd = ctx.saved_tensors
         if dy is None:   # only the stream was used
             return dh, dh, None, None
-        dx = torch.empty_like(h)
-        dgain = torch.empty(gain.shape, dtype=torch.float32, device=h.device) if ctx.needs_input_grad[2] else None
-        rmsnorm_backward(dy.contiguous(), h, gain, rstd, dx, dgain, dh=None if dh is None else dh.contiguous())
-        return dx, None if ctx.alone else dx, None if dgain is None else dgain.to(gain.dtype), None
+        grads = _RMSNormGrad.apply if torch.is_grad_enabled() else _norm_grads
+        dx, dgain = grads(dy, dh, h, gain, rstd, ctx.needs_input_grad[2])
+        return dx, None if ctx.alone else dx, dgain, None
+
+
+def _norm_grads(dy, dh, h, gain, rstd, want_gain):
+    dx = torch.empty_like(h)
+    dgain = torch.empty(gain.shape, dtype=torch.float32, device=h.device) if want_gain else None
+    rmsnorm_backward(dy.contiguous(), h, gain, rstd, dx, dgain, dh=None if dh is None else dh.contiguous())
+    return dx, None if dgain is None else dgain.to(gain.dtype)
+
+
+class _RMSNormGrad(torch.autograd.Function):
+    """The gradients under create_graph: connected to what they come from, so that differentiating them
+    again is refused instead of passing the norm over."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return _norm_grads(*args)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("RMSNorm can be differentiated once only: its gradients have no gradient")
 
 
 class RMSNorm(torch.nn.Module):
     """y = h / sqrt(mean(h^2) + eps) * gain over the last dimension (float32 or bfloat16), with h = x.
     With a residual of the same shape h = x + residual, rounded to their dtype, and forward returns
-    (y, h): h goes on as the residual stream.  gain is an ordinary parameter (float32)."""
+    (y, h): h goes on as the residual stream.  gain is an ordinary parameter (float32).  It can be
+    differentiated once: a second derivative raises."""
 
     def __init__(self, width: int, *, eps: float = 1e-6, device="cuda"):
         super().__init__()
