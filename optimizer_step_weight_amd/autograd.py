@@ -29,6 +29,13 @@ _STATES = {"adamw": "mv", "nadam": "mv", "radam": "mv", "lion": "m", "rmsprop": 
            "sgd": "", "sgd_momentum": "m"}
 
 
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """t as the library takes it, contiguous from a 16-byte aligned address: a copy where it is not (a
+    view into a larger tensor need not be)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _LinearStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x2d, anchor, layer):
@@ -40,9 +47,7 @@ class _LinearStep(torch.autograd.Function):
     def backward(ctx, dy):
         (x2d,) = ctx.saved_tensors
         layer = ctx.layer
-        dy = dy.contiguous()
-        if dy.dtype != layer.weight.dtype:
-            dy = dy.to(layer.weight.dtype)
+        dy = _packed(dy.to(layer.weight.dtype))
         layer.step_count += 1
         kw = dict(opt=layer.opt, hyper=layer.hyper, step=layer.step_count, seed=layer.seed,
                   m_scale=layer.m_scale, v_scale=layer.v_scale)
@@ -110,7 +115,7 @@ class FusedLinear(torch.nn.Module):
         if x.shape[-1] != self.in_features:
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         lead = x.shape[:-1]
-        x2d = x.reshape(-1, self.in_features).to(torch.bfloat16).contiguous()
+        x2d = _packed(x.reshape(-1, self.in_features).to(torch.bfloat16))
         y = _LinearStep.apply(x2d, self._anchor, self)
         return y.reshape(*lead, self.out_features)
 
@@ -131,7 +136,7 @@ class _ExpertsStep(torch.autograd.Function):
     def backward(ctx, dy):
         x2d, ends = ctx.saved_tensors
         layer = ctx.layer
-        dy = dy.contiguous().to(torch.bfloat16)
+        dy = _packed(dy.to(torch.bfloat16))
         layer.step_count += 1
         dx = None
         if ctx.needs_input_grad[0]:   # with the weights as they were
@@ -173,7 +178,7 @@ class FusedExperts(FusedLinear):
             raise ValueError(f"x must be [rows, {self.in_features}] (got {tuple(x.shape)})")
         if ends.numel() != self.experts:
             raise ValueError(f"ends must have {self.experts} entries (got {ends.numel()})")
-        return _ExpertsStep.apply(x.to(torch.bfloat16).contiguous(), self._anchor, ends, self)
+        return _ExpertsStep.apply(_packed(x.to(torch.bfloat16)), self._anchor, ends, self)
 
     def extra_repr(self) -> str:
         return f"experts={self.experts}, " + super().extra_repr()
@@ -204,7 +209,7 @@ class _RMSNorm(torch.autograd.Function):
 def _norm_grads(dy, dh, h, gain, rstd, want_gain):
     dx = torch.empty_like(h)
     dgain = torch.empty(gain.shape, dtype=torch.float32, device=h.device) if want_gain else None
-    rmsnorm_backward(dy.contiguous(), h, gain, rstd, dx, dgain, dh=None if dh is None else dh.contiguous())
+    rmsnorm_backward(_packed(dy), h, gain, rstd, dx, dgain, dh=None if dh is None else _packed(dh))
     return dx, None if dgain is None else dgain.to(gain.dtype)
 
 
@@ -237,8 +242,8 @@ class RMSNorm(torch.nn.Module):
             raise ValueError(f"expected last dimension {self.width}, got {x.shape[-1]}")
         if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
             raise ValueError("residual must have the shape and dtype of x")
-        flat = lambda t: t.reshape(-1, self.width).contiguous()  # noqa: E731
-        out = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), self.gain, self.eps)
+        flat = lambda t: _packed(t.reshape(-1, self.width))  # noqa: E731
+        out = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), _packed(self.gain), self.eps)
         return out.view(x.shape) if residual is None else tuple(t.view(x.shape) for t in out)
 
     def extra_repr(self) -> str:

@@ -67,3 +67,53 @@ def test_norm_gradients_of_either_output(A, use, frozen):
     exact = torch.autograd.grad(loss2, [x2, r2] + ([] if frozen or use == "h" else [w2]))
     for a, b in zip(want, exact):
         assert torch.allclose(a.double(), b, rtol=1e-5, atol=1e-5)
+
+
+def misplaced(t):
+    """The same values in a contiguous tensor whose data is not 16-byte aligned."""
+    out = torch.empty(t.numel() + 1, dtype=t.dtype)[1:].view(t.shape)
+    assert out.is_contiguous() and out.data_ptr() % 16 != 0
+    return out.copy_(t.detach())
+
+
+@pytest.mark.parametrize("where", ["x", "residual", "gain", "dy", "dh", "column slice"])
+def test_norm_of_views_that_are_not_aligned(A, where):
+    g = torch.Generator().manual_seed(3)
+    norm = A.RMSNorm(15, device="cpu")
+    x, r, dy, dh = (torch.randn(4, 15, generator=g) for _ in range(4))
+
+    def run(x, r, dy, dh):
+        x, r = x.detach().requires_grad_(True), r.detach().requires_grad_(True)
+        norm.gain.grad = None
+        y, h = norm(x, r)
+        torch.autograd.backward([y, h], [dy, dh])
+        return y, h, x.grad, r.grad, norm.gain.grad
+    want = run(x, r, dy, dh)
+    if where == "gain":
+        norm.gain = torch.nn.Parameter(misplaced(norm.gain))
+        assert norm.gain.data_ptr() % 16 != 0
+    moved = [misplaced(t) if n == where else t for n, t in (("x", x), ("residual", r), ("dy", dy), ("dh", dh))]
+    if where == "column slice":   # neither contiguous nor aligned
+        moved = [torch.cat([t[:, :1], t], 1)[:, 1:] for t in moved]
+    assert all(torch.equal(a, b) for a, b in zip(run(*moved), want))
+
+
+@pytest.mark.parametrize("layer", ["experts", "linear"])
+def test_trained_layers_of_views_that_are_not_aligned(A, monkeypatch, layer):
+    """Inputs and incoming gradients are copied where the library could not take them."""
+    seen = []
+
+    def take(*tensors, **kw):
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16:
+                assert t.data_ptr() % 16 == 0 and t.is_contiguous()
+        seen.append(len(tensors))
+    for name in ("grouped_gemm", "grouped_dgrad", "grouped_wgrad_step", "linear_backward_step"):
+        monkeypatch.setattr(A, name, take)
+    BF = torch.bfloat16
+    x, dy = torch.randn(6, 128).to(BF), torch.randn(6, 256).to(BF)
+    mod = A.FusedExperts(2, 128, 256, device="cpu") if layer == "experts" else A.FusedLinear(128, 256, device="cpu")
+    xm = misplaced(x).requires_grad_(True)
+    y = mod(xm, torch.tensor([2, 6], dtype=torch.int32)) if layer == "experts" else mod(xm)
+    y.backward(misplaced(dy))
+    assert len(seen) == (3 if layer == "experts" else 1) and xm.grad.shape == x.shape
