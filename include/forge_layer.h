@@ -32,7 +32,7 @@ extern "C" {
  *                    h may be x or residual itself (in place), else it overlaps no input.
  *   gain             [1, D], F32 or BF16.
  *   y                [T, D] F32, BF16 (nearest even) or FP8_E4M3.  FP8: y holds
- *                    rne_e4m3(clamp(y / scale, -448, 448)) with
+ *                    rne_e4m3(clamp(y / scale, -448, 448)), the quotients rounded to fp32, with
  *                      FORGE_SCALE_ROW     scale = max(amax_t |y| / 448, 2^-126), written to
  *                                          y->scale[t] (T fp32);
  *                      FORGE_SCALE_TENSOR  scale = y->scale[0], read (> 0): the per-tensor form

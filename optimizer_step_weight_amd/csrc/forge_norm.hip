@@ -153,6 +153,37 @@ __device__ __forceinline__ int cols_in(int c, int D) { return D - c < 0 ? 0 : D 
 // Clamped to the fp8 range; NaN stays.
 __device__ __forceinline__ float clamp8(float y) { return y > kFp8Max ? kFp8Max : (y < -kFp8Max ? -kFp8Max : y); }
 
+// y / scale, rounded once to fp32: the product with the inverse can be a step off and lie on the other
+// side of a tie between two codes, so it is corrected by its remainder (with it, the 1.2 thousand million
+// quotients of every 24-bit divisor that are next to a tie of e4m3 all equal the division's).  Two
+// operations an element; the division's own sequence would take 5 to 14 % of the kernel's time.
+// Factors of 2 keep the inverse and the remainder in range.
+struct Divisor {
+  float m, s, inv;
+  __device__ __forceinline__ explicit Divisor(float scale) {
+    const float mag = fabsf(scale);
+    m = mag < 0x1p-70f ? 0x1p80f : mag > 0x1p100f ? 0x1p-64f : 1.0f;
+    s = scale * m;
+    inv = 1.0f / s;
+    if (isinf(s)) s = 0.0f;  // finite ones give zero, infinite ones NaN
+  }
+  // (y m) / (scale m).  BOUNDED: |y / scale| is no more than a step over 448, or not finite by the scale.
+  template <bool BOUNDED>
+  __device__ __forceinline__ float into(float y) const {
+    const float q = y * inv, r = __builtin_fmaf(q, s, -y), c = __builtin_fmaf(-r, inv, q);
+    if constexpr (BOUNDED) return c;
+    else return fabsf(q) < 1024.0f ? c : q;
+  }
+};
+
+// The quotient clamped to the fp8 range.  By the row's own scale it is a step over 448 at most, which
+// the conversion rounds to 448.
+template <bool ROW>
+__device__ __forceinline__ float quotient8(float y, const Divisor& d) {
+  if constexpr (ROW) return d.into<true>(y);
+  else return clamp8(d.into<false>(y));
+}
+
 // Larger of two magnitudes; NaN wins.
 __device__ __forceinline__ float amax2(float a, float b) { return (a > b || a != a) ? a : b; }
 
@@ -248,17 +279,24 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
         if (!ODD || j < in[i]) mx = amax2(mx, fabsf(v[i][j]));
       }
     }
-    float inv = 1.0f;
+    float scale = 1.0f;
     if constexpr (YT == FORGE_Y_FP8_ROW) {
       mx = row_reduce<Max, TPR>(mx, red[par][1]);
-      float scale = mx * (1.0f / kFp8Max);
+      scale = mx / kFp8Max;
       scale = scale < kScaleMin ? kScaleMin : scale;
       if (lane == 0) a.y_scale[row] = scale;
-      inv = 1.0f / scale;
     } else if constexpr (YT == FORGE_Y_FP8_TENSOR) {
-      inv = 1.0f / a.y_scale[0];
+      scale = a.y_scale[0];
     }
     top = amax2(top, mx);
+    const Divisor d(scale);
+    // a wave has one row, and a row one scale
+    if (YT != FORGE_Y_F32 && YT != FORGE_Y_BF16 && __builtin_amdgcn_readfirstlane(__float_as_int(d.m)) != 0x3F800000)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= d.m;
+    auto code = [&](float y) { return quotient8<YT == FORGE_Y_FP8_ROW>(y, d); };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
@@ -270,8 +308,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormArgs
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           int w = 0;
-          w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(v[i][4 * j] * inv), clamp8(v[i][4 * j + 1] * inv), w, false);
-          w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(v[i][4 * j + 2] * inv), clamp8(v[i][4 * j + 3] * inv), w, true);
+          w = __builtin_amdgcn_cvt_pk_fp8_f32(code(v[i][4 * j]), code(v[i][4 * j + 1]), w, false);
+          w = __builtin_amdgcn_cvt_pk_fp8_f32(code(v[i][4 * j + 2]), code(v[i][4 * j + 3]), w, true);
           q[j] = (uint32_t)w;
         }
         uint8_t* y = static_cast<uint8_t*>(a.y) + at;
@@ -314,26 +352,26 @@ __global__ __launch_bounds__(256) void rmsnorm_loop_kernel(NormArgs a) {
   const float s = 1.0f / sqrtf(__builtin_fmaf(ss, 1.0f / (float)a.D, a.eps));
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = s;
   auto y_at = [&](int64_t c) { return (load1<BF>(hp, base + c) * s) * gain1(a.gain, a.gain_bf16, c); };
-  float mx = 0.0f, inv = 1.0f;
+  float mx = 0.0f, scale = 1.0f;
   if (YT == FORGE_Y_FP8_ROW || a.amax) {
     for (int64_t c = threadIdx.x; c < a.D; c += 256) mx = amax2(mx, fabsf(y_at(c)));
     mx = row_reduce<Max, 256>(mx, red[1]);
     if (a.amax && threadIdx.x == 0) raise_amax(a.amax, mx);
   }
   if constexpr (YT == FORGE_Y_FP8_ROW) {
-    float scale = mx * (1.0f / kFp8Max);
+    scale = mx / kFp8Max;
     scale = scale < kScaleMin ? kScaleMin : scale;
     if (threadIdx.x == 0) a.y_scale[blockIdx.x] = scale;
-    inv = 1.0f / scale;
   } else if constexpr (YT == FORGE_Y_FP8_TENSOR) {
-    inv = 1.0f / a.y_scale[0];
+    scale = a.y_scale[0];
   }
+  const Divisor d(scale);
   for (int64_t c = threadIdx.x; c < a.D; c += 256) {
     const float y = y_at(c);
     if constexpr (YT == FORGE_Y_F32 || YT == FORGE_Y_BF16) {
       store1<YT == FORGE_Y_BF16>(a.y, base + c, y);
     } else {
-      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp8(y * inv), 0.0f, 0, false);
+      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient8<YT == FORGE_Y_FP8_ROW>(y * d.m, d), 0.0f, 0, false);
       static_cast<uint8_t*>(a.y)[base + c] = (uint8_t)(w & 0xFF);
     }
   }

@@ -107,3 +107,82 @@ def test_fp8_product_of_scales_whose_product_leaves_fp32(lib):
     s = xs.to(R.F64)[:, None] * ws[0].to(R.F64)[None]
     want = (X.to(R.F64) @ W[0].to(R.F64).t()) * s
     near(Y, want, (HALF[BF] + 4 * R.U) * want.abs() + 2.0 ** -134)   # equal products: the sum is exact
+
+
+# ------------------------------------------------------------------ fp8 outputs of the norm
+def fp8_halfway():
+    """Every value halfway between two neighbouring finite codes of e4m3, and the codes."""
+    v = torch.arange(0, 0x7F, dtype=torch.uint8).view(FP8).to(R.F64)
+    return torch.cat([(v[1:] + v[:-1]) / 2, v])
+
+
+def beside(mid, scale):
+    """fp32 numbers at mid * scale and one and two steps to either side, both signs."""
+    y = (mid * float(scale)).float()
+    steps = [y]
+    for _ in range(2):
+        steps += [torch.nextafter(steps[-1], torch.tensor(float("inf")))]
+    low = y
+    for _ in range(2):
+        low = torch.nextafter(low, torch.tensor(0.0))
+        steps += [low]
+    out = torch.cat(steps)
+    return torch.cat([out, -out])
+
+
+def unit_rows(lib, gain, **kw):
+    """fp8 codes of y = gain: rows of ones and minus ones, whose norm is 1 exactly."""
+    D = gain.numel()
+    x = torch.ones(3, D)
+    x[1] = -1.0
+    rstd, y = torch.empty(3, device="cuda"), torch.empty(3, D, dtype=FP8, device="cuda")
+    lib.rmsnorm(x.cuda(), gain.cuda(), y, rstd=rstd, eps=0.0, **kw)
+    assert bool((rstd == 1.0).all())
+    return y.cpu()
+
+
+def as_codes(q):
+    return q.clamp(-448, 448).to(FP8).view(torch.uint8)
+
+
+@pytest.mark.parametrize("D", [2048, 4096, 8192, 3001, 32768])
+def test_norm_divides_by_the_scale(lib, D):
+    """rne_e4m3 of the fp32 quotient, for quotients beside every tie, and for scales whose inverse is no number."""
+    g = gen(D)
+    for scale in [0.0123, 1.7, 3.3e-5, 2.0 ** -126, 2.0 ** -135, 3.0e38] + torch.rand(6, generator=g).tolist():
+        s = torch.tensor([scale])
+        gain = beside(fp8_halfway(), s)
+        gain = torch.where(gain.isfinite(), gain, 0.0).repeat(-(-D // gain.numel()))[:D].contiguous()
+        y = unit_rows(lib, gain, y_scale=s.cuda(), scale_mode="tensor")
+        want = as_codes(gain / s)
+        for row, sign in ((0, 1), (1, -1)):
+            assert torch.equal(y[row].view(torch.uint8), as_codes(sign * gain / s)), (scale, row)
+        assert torch.equal(y[2].view(torch.uint8), want)
+
+
+@pytest.mark.parametrize("D", [2048, 4096, 8192, 3001, 32768])
+def test_norm_row_scale_is_the_quotient(lib, D):
+    g = gen(D + 1)
+    for top in torch.rand(6, generator=g).tolist() + [448.0, 1e-30, 1e30]:
+        top = torch.tensor(top)
+        scale = top / 448
+        gain = beside(fp8_halfway(), scale).clamp(-top, top).repeat(-(-D // 2540))[:D].contiguous()
+        gain[D // 3] = top
+        sc = torch.empty(3, device="cuda")
+        y = unit_rows(lib, gain, y_scale=sc)
+        assert bool((sc.cpu() == scale).all()), (float(top), sc, float(scale))
+        assert torch.equal(y[0].view(torch.uint8), as_codes(gain / scale)), float(top)
+        assert torch.equal(y[1].view(torch.uint8), as_codes(-gain / scale)), float(top)
+
+
+@pytest.mark.parametrize("D", [64, 4096, 32768])
+def test_norm_infinite_rows_to_fp8(lib, D):
+    """An infinite y makes the row's scale infinite: the finite ones give zero, it gives NaN."""
+    gain = torch.ones(D)
+    gain[5], gain[7] = float("inf"), -float("inf")
+    sc = torch.empty(3, device="cuda")
+    y = unit_rows(lib, gain, y_scale=sc).float()
+    assert torch.isinf(sc).all() and torch.isnan(y[:, [5, 7]]).all()
+    keep = torch.ones(D, dtype=torch.bool)
+    keep[[5, 7]] = False
+    assert bool((y[:, keep] == 0).all())
