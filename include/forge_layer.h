@@ -50,9 +50,9 @@ forge_status forge_rmsnorm(const forge_tensor* x, const forge_tensor* residual, 
 
 /*
  * forge_rmsnorm_backward -- gradients of forge_rmsnorm (unquantised y) for one upstream dy:
- *     a  = dy * gain
- *     dx = rstd * a - h * (rstd^3 * mean(a * h)) + dh     (the gradient of x and of residual)
- *     dgain[d] = sum_t dy * h * rstd
+ *     a  = dy * gain,  u = h * rstd
+ *     dx = rstd * (a - u * mean(a * u)) + dh     (the gradient of x and of residual)
+ *     dgain[d] = sum_t dy * u
  *   dy, dh, h, dx    [T, D], all F32 or all BF16; dh (the gradient arriving on h itself) may be
  *                    NULL.  dx may be dy or dh itself, else it overlaps no input.
  *   rstd             T fp32, as forge_rmsnorm wrote it.

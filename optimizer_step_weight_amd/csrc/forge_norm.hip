@@ -2,7 +2,8 @@
 //
 // h = x + r (rounded to the stream's dtype), s = 1 / sqrt(mean(h^2) + eps), y = (h s) gain, and
 // for fp8 rne(y / scale) with the row's scale amax / 448 or a given one.  Backward, with
-// a = dy gain and c = mean(a h): dx = s a - h s^3 c + dh, dgain = sum over rows of dy h s.
+// a = dy gain, u = h s and c = mean(a u): dx = s (a - u c) + dh, dgain = sum over rows of dy u.  No power
+// of s is formed: its cube leaves fp32 for rows of an rms of 10^13 or 10^-13.
 //
 // Both are bound by memory: every element is read and written once.  A row is held in the
 // registers of one wave (D <= 2048) or of one workgroup of 256 or 512 threads (D <= 16384), 8
@@ -432,11 +433,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(Norm
       if constexpr (DH && AHEAD) unpack8<BF>(rdh[i], dh[i]);
       if (!AHEAD) fetch_gain(i);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c = __builtin_fmaf(dy[i][j] * gain[i][j], h[i][j], c);
+      for (int j = 0; j < 8; ++j) {
+        h[i][j] *= s;
+        c = __builtin_fmaf(dy[i][j] * gain[i][j], h[i][j], c);
+      }
     }
     if (AHEAD && row + 1 < end) fetch(row + 1);
     c = row_reduce<Sum, TPR>(c, red[par]);
-    const float k = (s * s * s) * (c * inv_d);
+    c *= inv_d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!in[i]) continue;
@@ -447,9 +451,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(Norm
       float dx[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dx[j] = __builtin_fmaf(s, dy[i][j] * gain[i][j], -(h[i][j] * k));
+        dx[j] = s * __builtin_fmaf(-h[i][j], c, dy[i][j] * gain[i][j]);
         if constexpr (DH) dx[j] += dh[i][j];
-        if constexpr (DG) acc[i][j] = __builtin_fmaf(dy[i][j], h[i][j] * s, acc[i][j]);
+        if constexpr (DG) acc[i][j] = __builtin_fmaf(dy[i][j], h[i][j], acc[i][j]);
       }
       store_cols<BF, ODD>(a.dx, row * a.D + (lane + i * TPR) * 8, dx, in[i]);
     }
@@ -473,15 +477,14 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_loop_kernel(NormBwdArgs a, in
     const float s = a.rstd[row];
     float sum = 0.0f;
     for (int64_t c = threadIdx.x; c < a.D; c += 256)
-      sum = __builtin_fmaf(load1<BF>(a.dy, base + c) * gain1(a.gain, a.gain_bf16, c), load1<BF>(a.h, base + c), sum);
-    sum = row_reduce<Sum, 256>(sum, red[par]);
-    const float k = (s * s * s) * (sum * (1.0f / (float)a.D));
+      sum = __builtin_fmaf(load1<BF>(a.dy, base + c) * gain1(a.gain, a.gain_bf16, c), load1<BF>(a.h, base + c) * s, sum);
+    const float mean = row_reduce<Sum, 256>(sum, red[par]) * (1.0f / (float)a.D);
     for (int64_t c = threadIdx.x; c < a.D; c += 256) {
-      const float dy = load1<BF>(a.dy, base + c), h = load1<BF>(a.h, base + c);
-      float dx = __builtin_fmaf(s, dy * gain1(a.gain, a.gain_bf16, c), -(h * k));
+      const float dy = load1<BF>(a.dy, base + c), u = load1<BF>(a.h, base + c) * s;
+      float dx = s * __builtin_fmaf(-u, mean, dy * gain1(a.gain, a.gain_bf16, c));
       if (a.dh) dx += load1<BF>(a.dh, base + c);
       store1<BF>(a.dx, base + c, dx);
-      if (a.dgain) part[c] = __builtin_fmaf(dy, h * s, part[c]);
+      if (a.dgain) part[c] = __builtin_fmaf(dy, u, part[c]);
     }
   }
 }

@@ -186,3 +186,26 @@ def test_norm_infinite_rows_to_fp8(lib, D):
     keep = torch.ones(D, dtype=torch.bool)
     keep[[5, 7]] = False
     assert bool((y[:, keep] == 0).all())
+
+
+# ------------------------------------------------------------------ the norm's gradient far from one
+@pytest.mark.parametrize("D", [64, 130, 512, 2048, 4100, 8192, 16384, 16392])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_norm_backward_of_rows_far_from_one(lib, D, dt):
+    """The cube of 1 / rms leaves fp32's range long before the gradient does.  eps = 0."""
+    T = 9
+    g = gen(D)
+    scale = torch.tensor([1e14, 1e-14, 1e18, 1e-18, 1.0, 1e13, 1e-13, 1e12, 1e-12])[:, None]
+    x, dy, gain = (torch.randn(T, D, generator=g) * scale).to(dt), torch.randn(T, D, generator=g), 1 + 0.3 * torch.randn(D, generator=g)
+    dy[:, ::2] += 2.0                     # so that the part along h is as large as the rest
+    x[:, ::2] = x[:, ::2].abs()
+    dy, dh = dy.to(dt), (torch.randn(T, D, generator=g) / scale).to(dt)
+    rstd = R.norm(x, gain, 0.0)[1].float()
+    a, s, hh = (dy.to(R.F64) * gain.to(R.F64)).abs(), rstd.to(R.F64)[:, None], x.to(R.F64).abs()
+    for with_dh in (False, True):
+        dx, dgain = R.norm_grads(dy, x, gain, rstd, dh if with_dh else None)
+        mag = s * a + hh * s ** 3 * (a * hh).mean(1, keepdim=True) + (dh.to(R.F64).abs() if with_dh else 0)
+        o, og = torch.empty(T, D, dtype=dt, device="cuda"), torch.empty(D, device="cuda")
+        lib.rmsnorm_backward(dy.cuda(), x.cuda(), gain.cuda(), rstd.cuda(), o, og, dh=dh.cuda() if with_dh else None)
+        near(o, dx, (-(-D // 64) + 46) * R.U * mag + HALF[dt] * dx.abs() + 2.0 ** -133)
+        near(og, dgain, (T + 16 + 4) * R.U * (dy.to(R.F64).abs() * hh * s).sum(0) + 2.0 ** -140)
