@@ -88,12 +88,12 @@ def _lib():
                   "forge_linear_backward_step_fused_noalloc", "forge_wgrad_gemm", "forge_optimizer_step",
                   "forge_step_scalars", "forge_device_check"):
             getattr(L, f).restype = st
-        from . import _build, layer
+        from . import _build, _layer_abi
         built, want = L.forge_build_id().decode(), _build.source_hash()
         if built != want:
             raise ImportError(f"{LIB_PATH} was built from other sources (build id {built}, sources {want}); "
                               "rebuild it with __graft_entry__.build()")
-        layer._declare(L)
+        _layer_abi.declare(L)
         _lib_handle = L
     return _lib_handle
 

@@ -114,3 +114,16 @@ def test_hyper_parameters_changed_in_place_are_read_again(f, monkeypatch, kind):
     assert call(d) == [0.5]
     d["lr"] = 0.25
     assert call(d) == [0.25]
+
+
+def test_host_calls_need_no_torch():
+    """Versions, scalars and refusals of the C ABI in a process that has no torch."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import optimizer_step_weight_amd as f\n"
+            "assert f.version() > 0 and f.build_id() and f.step_scalars('adamw', {'lr': 0.5}, 1)['lr'] == 0.5\n"
+            "assert f._lib().forge_rmsnorm(None, None, None, 0.0, None, None, 0, None, None, None) == 1 and f.last_error()\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
