@@ -31,7 +31,7 @@ def gen(seed):
 
 def near(got, want, tol):
     """|got - want| <= tol element by element (64-bit tensors of one device)."""
-    bad = (got.to(want.device).to(R.F64) - want).abs() - tol
+    bad = (got.detach().to(want.device).to(R.F64) - want).abs() - tol
     assert not torch.isnan(bad).any() and float(bad.max()) <= 0, f"over by {float(bad.max())}"
 
 
@@ -209,3 +209,140 @@ def test_norm_backward_of_rows_far_from_one(lib, D, dt):
         lib.rmsnorm_backward(dy.cuda(), x.cuda(), gain.cuda(), rstd.cuda(), o, og, dh=dh.cuda() if with_dh else None)
         near(o, dx, (-(-D // 64) + 46) * R.U * mag + HALF[dt] * dx.abs() + 2.0 ** -133)
         near(og, dgain, (T + 16 + 4) * R.U * (dy.to(R.F64).abs() * hh * s).sum(0) + 2.0 ** -140)
+
+
+# ------------------------------------------------------------------ several rows for a workgroup
+def chain(D):
+    return -(-D // 64) + 40
+
+
+def many_rows(T, D, dt, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    size = torch.exp2(torch.randint(-6, 7, (T, 1), generator=g, device="cuda").float())   # a row mistaken for another shows
+    return (new(T, D) * size).to(dt), new(T, D).to(dt), new(T, D).to(dt), 1 + 0.3 * new(D)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,D", [(17000, 130), (17001, 512), (16500, 1024), (17000, 2047), (5000, 2056), (4200, 4096), (4999, 4099),
+                                 (4200, 5120), (4500, 8192), (5000, 8200), (4300, 16384), (300, 16392)])
+def test_norm_walks_over_rows(lib, T, D, dt):
+    """Three rows at least for a workgroup: the next row's loads, in-place h beside them, scales and amax."""
+    eps = 1e-5
+    x, r, _, gain = many_rows(T, D, dt, D)
+    h = (x.float() + r.float()).to(dt)
+    want, rstd = R.norm(h, gain, eps)
+    tol = chain(D) * R.U
+    for alias in ("x", "residual"):
+        a, b = x.clone(), r.clone()
+        y, sc, am, s = torch.empty(T, D, dtype=FP8, device="cuda"), torch.empty(T, device="cuda"), torch.zeros(1, device="cuda"), torch.empty(T, device="cuda")
+        lib.rmsnorm(a, gain, y, residual=b, h=a if alias == "x" else b, rstd=s, y_scale=sc, amax=am, eps=eps)
+        assert torch.equal(a if alias == "x" else b, h)
+        near(s, rstd, tol * rstd)
+        near(am, want.abs().max().view(1), tol * want.abs().max())
+        scale = want.abs().amax(1) / 448
+        near(sc, scale, (tol + R.U) * scale)
+        s64 = sc.to(R.F64)[:, None]
+        near(y.to(R.F64) * s64, want, (HALF[FP8] + tol + 3 * R.U) * want.abs() + 2.0 ** -10 * s64)
+    y = torch.empty(T, D, dtype=dt, device="cuda")
+    want, rstd = R.norm(x, gain, eps)
+    lib.rmsnorm(x, gain, y, eps=eps)
+    near(y, want, (tol + HALF[dt]) * want.abs() + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,D", [(4500, 64), (4500, 130), (4400, 512), (4200, 2048), (3300, 4096), (2500, 4099), (2500, 4104), (3400, 8192),
+                                 (2500, 8193), (2500, 8200), (2200, 16384), (2100, 16383), (2200, 16392)])
+def test_norm_backward_walks_over_rows(lib, T, D, dt):
+    h, dy, dh, gain = many_rows(T, D, dt, D + 1)
+    rstd = R.norm(h, gain, 1e-5)[1].float()
+    for with_dh in (False, True):
+        dx, dgain = R.norm_grads(dy, h, gain, rstd, dh if with_dh else None)
+        a, s, hh = (dy.to(R.F64) * gain.to(R.F64)).abs(), rstd.to(R.F64)[:, None], h.to(R.F64).abs()
+        mag = s * a + hh * s ** 3 * (a * hh).mean(1, keepdim=True) + (dh.to(R.F64).abs() if with_dh else 0)
+        o, og = torch.empty_like(h), torch.full((D,), float("nan"), device="cuda")
+        lib.rmsnorm_backward(dy, h, gain, rstd, o, og, dh=dh if with_dh else None)
+        near(o, dx, (chain(D) + 6) * R.U * mag + HALF[dt] * dx.abs() + 2.0 ** -133)
+        near(og, dgain, (-(-T // 1024) + 1024 // 16 + 16 + 4) * R.U * (dy.to(R.F64).abs() * hh * s).sum(0) + 2.0 ** -140)
+        o2 = dh.clone() if with_dh else dy.clone()      # in place, without the gain's gradient
+        lib.rmsnorm_backward(dy if with_dh else o2, h, gain, rstd, o2, dh=o2 if with_dh else None)
+        assert torch.equal(o, o2)
+
+
+# ------------------------------------------------------------------ outputs past 2^31 elements
+def some(shape, seed):
+    return torch.randint(-2, 3, shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(BF)
+
+
+def test_input_gradient_past_2_31_elements(lib):
+    T, N, K, ends = 132_000, 128, 16384, [66_001, 132_000]
+    dY, W = some((T, N), 1), some((2, N, K), 2)
+    dX = torch.empty(T, K, dtype=BF, device="cuda")
+    lib.grouped_dgrad(dY, W, torch.tensor(ends, dtype=torch.int32, device="cuda"), dX)
+    for a, b, e in ((0, 64, 0), (65_950, 66_001, 0), (66_001, 66_050, 1), (131_071, 131_200, 1), (T - 70, T, 1)):
+        assert torch.equal(dX[a:b].cpu(), (dY[a:b].cpu().double() @ W[e].cpu().double()).to(BF))
+
+
+def test_weight_gradient_and_step_past_2_31_elements(lib):
+    """The last experts of 2^31 weights and more: gradients at offsets past 2^31, the step's past 2^32 bytes."""
+    E, N, K, T = 33, 8192, 8192, 70
+    X, dY = some((T, K), 3), some((T, N), 4)
+    ends = torch.full((E,), 30, dtype=torch.int32)
+    ends[-1] = T                                  # the first and the last expert have rows
+    dW = torch.empty(E, N, K, device="cuda")
+    lib.grouped_wgrad(X, dY, ends.cuda(), dW)
+    for e, (a, b) in ((0, (0, 30)), (16, (30, 30)), (E - 1, (30, T))):
+        for n in (0, 4000, N - 40):
+            want = dY[a:b, n:n + 40].cpu().double().t() @ X[a:b].cpu().double()
+            assert torch.equal(dW[e, n:n + 40].cpu(), want.float())
+    W = torch.zeros(E, N, K, dtype=BF, device="cuda")
+    lib.grouped_wgrad_step(X, dY, ends.cuda(), W, opt="sgd", hyper={"lr": 1.0}, step=1, seed=1, sr=False)
+    assert torch.equal(W[0], (-dW[0]).to(BF)) and torch.equal(W[-1], (-dW[-1]).to(BF)) and not bool(W[1:-1].any())
+
+
+# ------------------------------------------------------------------ the layers
+def test_norm_layer_in_bf16_with_a_frozen_gain(lib):
+    """Views that are not aligned, either output alone, no gradient of the gain."""
+    from optimizer_step_weight_amd.autograd import RMSNorm
+    T, D = 37, 1023
+    x, r, dy, gain = many_rows(T, D, BF, 7)
+    dh = r.flip(0).contiguous()
+    norm = RMSNorm(D)
+    norm.gain.data.copy_(gain)
+    norm.gain.requires_grad_(False)
+    pad = lambda t: torch.cat([t[:1], t])[1:].requires_grad_(True)  # noqa: E731
+    xi, ri = pad(x).detach().requires_grad_(True), pad(r).detach().requires_grad_(True)
+    assert xi.data_ptr() % 16 and xi.is_contiguous()
+    hw = (x.float() + r.float()).to(BF)
+    want, rstd = R.norm(hw, gain, 1e-6)
+    s32 = rstd.float()
+    for use in ("both", "y", "h"):
+        xi.grad = ri.grad = None
+        y, h = norm(xi, ri)
+        assert torch.equal(h, hw)
+        near(y, want, (chain(D) * R.U + HALF[BF]) * want.abs() + 2.0 ** -133)
+        ins = [dy if use != "h" else None, dh if use != "y" else None]
+        torch.autograd.backward([t for t, g in zip((y, h), ins) if g is not None], [torch.cat([g[:1], g])[1:] for g in ins if g is not None])
+        if use == "h":
+            assert torch.equal(xi.grad, dh) and torch.equal(ri.grad, dh)
+            continue
+        dx = R.norm_grads(dy, hw, gain, s32, ins[1])[0]
+        a, s, hh = (dy.to(R.F64) * gain.to(R.F64)).abs(), rstd[:, None], hw.to(R.F64).abs()
+        mag = s * a + hh * s ** 3 * (a * hh).mean(1, keepdim=True) + (0 if ins[1] is None else dh.to(R.F64).abs())
+        near(xi.grad, dx, (3 * chain(D) + 8) * R.U * mag + HALF[BF] * dx.abs() + 2.0 ** -133)   # rstd is the kernel's own
+        assert torch.equal(xi.grad, ri.grad) and norm.gain.grad is None
+
+
+@pytest.mark.parametrize("opt", ["adamw", "lion"])
+def test_experts_with_8bit_moments(lib, opt):
+    from optimizer_step_weight_amd.autograd import FusedExperts
+    E, K, N, T = 3, 256, 384, 150
+    x, dy, W = some((T, K), 5), some((T, N), 6), (0.05 * some((E, N, K), 7).float()).to(BF)
+    ends = torch.tensor([40, 40, 140], dtype=torch.int32, device="cuda")
+    layer = FusedExperts(E, K, N, opt=opt, hyper={"lr": 1e-2}, seed=5, weight=W.clone(), state_dtype="int8")
+    m, ms, v, vs = (None if t is None else t.clone() for t in (layer.m, layer.m_scale, layer.v, layer.v_scale))
+    for step in (1, 2):
+        layer(x, ends).backward(dy)
+        lib.grouped_wgrad_step(x, dy, ends, W, m, v, opt=opt, hyper={"lr": 1e-2}, step=step, seed=5, m_scale=ms, v_scale=vs)
+    for a, b in ((layer.weight, W), (layer.m, m), (layer.m_scale, ms), (layer.v, v), (layer.v_scale, vs)):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
