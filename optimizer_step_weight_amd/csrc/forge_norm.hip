@@ -490,22 +490,27 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_loop_kernel(NormBwdArgs a, in
 }
 
 // dgain[c] = sum over the groups' partial rows, in a fixed order: thread (x, y) of 32 x 16 adds
-// rows y, y + 16, ..., then the 16 sums are added in order.
-__global__ __launch_bounds__(512) void dgain_kernel(const float* partial, float* dgain, int64_t groups, int D) {
+// rows y, y + 16, ..., then the 16 sums are added in order.  A workgroup takes 32 columns, and further
+// ones where D has more than a grid may (2^32 threads).
+constexpr int kGainBlocks = 1 << 16;
+__global__ __launch_bounds__(512) void dgain_kernel(const float* partial, float* dgain, int64_t groups, int64_t D) {
   __shared__ float part[16][33];
   const int x = (int)threadIdx.x & 31, y = (int)threadIdx.x >> 5;
-  const int c = (int)blockIdx.x * 32 + x;
-  float s = 0.0f;
-  if (c < D) {
+  for (int64_t c0 = (int64_t)blockIdx.x * 32; c0 < D; c0 += (int64_t)kGainBlocks * 32) {
+    const int64_t c = c0 + x;
+    float s = 0.0f;
+    if (c < D) {
 #pragma unroll 8
-    for (int64_t g = y; g < groups; g += 16) s += partial[g * D + c];
-  }
-  part[y][x] = s;
-  __syncthreads();
-  if (y == 0 && c < D) {
+      for (int64_t g = y; g < groups; g += 16) s += partial[g * D + c];
+    }
+    part[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < D) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += part[i][x];
-    dgain[c] = s;
+      for (int i = 1; i < 16; ++i) s += part[i][x];
+      dgain[c] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -602,8 +607,9 @@ int launch_rmsnorm_backward(int bf16, const NormBwdArgs& a, void* stream) {
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || !a.dgain) return (int)err;
-  hipLaunchKernelGGL(dgain_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(512), 0, st, a.partial, a.dgain, groups,
-                     a.D);
+  const int64_t blocks = ((int64_t)a.D + 31) / 32;
+  hipLaunchKernelGGL(dgain_kernel, dim3((unsigned)(blocks < kGainBlocks ? blocks : kGainBlocks)), dim3(512), 0, st, a.partial,
+                     a.dgain, groups, (int64_t)a.D);
   return (int)hipGetLastError();
 }
 

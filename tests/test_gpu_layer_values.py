@@ -346,3 +346,22 @@ def test_experts_with_8bit_moments(lib, opt):
         lib.grouped_wgrad_step(x, dy, ends, W, m, v, opt=opt, hyper={"lr": 1e-2}, step=step, seed=5, m_scale=ms, v_scale=vs)
     for a, b in ((layer.weight, W), (layer.m, m), (layer.m_scale, ms), (layer.v, v), (layer.v_scale, vs)):
         assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+
+
+@pytest.mark.parametrize("D", [2 ** 31 - 1, 2 ** 31 - 33])
+def test_gain_gradient_of_the_widest_rows(lib, D):
+    """More columns than threads of a grid, numbers next to 2^31 (no rows: the gradient is zero, the test short)."""
+    empty = torch.empty(0, D, dtype=BF, device="cuda")
+    gain, dgain = torch.ones(D, dtype=BF, device="cuda"), torch.full((D,), float("nan"), device="cuda")
+    lib.rmsnorm_backward(empty, empty, gain, torch.empty(0, device="cuda"), empty, dgain)
+    assert not bool(dgain.any())
+
+
+def test_gain_gradient_of_more_columns_than_a_grid_takes_at_once(lib):
+    T, D = 3, 2 ** 21 + 4099
+    h, dy, _, gain = many_rows(T, D, F32, 3)
+    rstd = R.norm(h, gain, 1e-5)[1].float()
+    dx, dgain = torch.empty_like(h), torch.full((D,), float("nan"), device="cuda")
+    lib.rmsnorm_backward(dy, h, gain, rstd, dx, dgain)
+    want = R.norm_grads(dy, h, gain, rstd)[1]
+    near(dgain, want, (T + 16 + 4) * R.U * (dy.double().abs() * h.double().abs() * rstd.double()[:, None]).sum(0) + 2.0 ** -140)
