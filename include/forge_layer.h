@@ -101,7 +101,7 @@ forge_status forge_grouped_wgrad_step(const forge_tensor* X, const forge_tensor*
 /*
  * One optimizer step over many tensors in one launch (parameters with a materialised gradient:
  * norm gains, biases, embeddings, weights of any size).  A tensor is n consecutive elements,
- * 0 <= n <= 2^32 - 8192; the moments of all tensors of a table are fp32, or all 8-bit in blocks of 64 of
+ * 0 <= n <= 2^32 - 8192, all together fewer than 2^36; the moments of all tensors of a table are fp32, or all 8-bit in blocks of 64 of
  * the same map (I8_B64 / U8_B64 or I8DYN_B64 / U8DYN_B64, ceil(n / 64) fp32 scales each; the
  * last block may be short).
  */

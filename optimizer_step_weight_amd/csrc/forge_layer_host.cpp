@@ -357,7 +357,7 @@ int64_t forge_multi_table_bytes(const forge_multi_tensor* tensors, int32_t n_ten
   for (int32_t i = 0; i < n_tensors; ++i) {
     if (tensors[i].n < 0 || tensors[i].n > (int64_t(1) << 32) - 8192) return -1;
     chunks += multi_chunks(tensors[i].n);
-    if (chunks >= (int64_t(1) << 31)) return -1;
+    if (chunks >= forge::kMultiMaxChunks) return -1;
   }
   return (int64_t)n_tensors * (int64_t)sizeof(forge::MultiEntry) + 4 * chunks;
 }
@@ -479,7 +479,7 @@ forge_status forge_multi_step(const forge_multi_info* info, const void* table, c
   if (!info) return fail(FORGE_ERR_ARG, "info is NULL");
   if (info->opt < FORGE_ADAMW || info->opt > FORGE_SGD_MOMENTUM)
     return fail(FORGE_ERR_ARG, "unknown optimizer %d", (int)info->opt);
-  if (info->tensors < 0 || info->chunks < 0 || info->chunks >= (int64_t(1) << 31) || info->groups < 0 ||
+  if (info->tensors < 0 || info->chunks < 0 || info->chunks >= forge::kMultiMaxChunks || info->groups < 0 ||
       info->groups > forge::kMultiGroups ||
       info->bytes != info->tensors * (int64_t)sizeof(forge::MultiEntry) + 4 * info->chunks)
     return fail(FORGE_ERR_ARG, "info is not one that forge_multi_pack wrote");

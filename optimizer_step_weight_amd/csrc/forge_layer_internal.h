@@ -75,6 +75,7 @@ int launch_grouped_step(int s_type, int opt, const GroupedWgradArgs& a, const Ep
 // ------------------------------------------------------------------ the step over many tensors
 constexpr int kMultiChunk = 4096;   // elements of a workgroup
 constexpr int kMultiGroups = 8;
+constexpr int64_t kMultiMaxChunks = int64_t(1) << 24;  // of 256 threads: a grid has fewer than 2^32
 struct MultiEntry {
   void* W;
   const void* g;

@@ -228,3 +228,16 @@ def test_norm_gradient_formula_against_differences():
             num.view(-1)[i] = (at(up) - at(down)) / (2 * eps)
         # central differences: O(eps^2) truncation and 2^-53 |loss| / eps rounding
         assert torch.allclose(grad, num, rtol=0, atol=1e-8)
+
+
+def test_multi_pack_refuses_more_chunks_than_a_grid_takes(f):
+    """2^32 threads of a launch, 256 a chunk of 4096 elements: 2^36 elements are refused when they are packed."""
+    from optimizer_step_weight_amd.layer import _MultiTensor
+    n = 2 ** 32 - 8192
+
+    def size(count):
+        a = (_MultiTensor * count)(*[_MultiTensor(FAKE + 64 * i * GB, FAKE - 64 * GB, None, None, None, None, n, 7, f.BF16, f.BF16, 0, 0)
+                                     for i in range(count)])
+        return f._lib().forge_multi_table_bytes(a, count)
+    assert size(16) == 16 * 72 + 16 * 4 * (2 ** 20 - 2)
+    assert size(17) == -1
