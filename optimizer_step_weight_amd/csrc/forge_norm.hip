@@ -151,38 +151,31 @@ __device__ __forceinline__ void store_cols(void* p, int64_t i, const float (&v)[
 }
 __device__ __forceinline__ int cols_in(int c, int D) { return D - c < 0 ? 0 : D - c > 8 ? 8 : D - c; }
 
-// Clamped to the fp8 range; NaN stays.
-__device__ __forceinline__ float clamp8(float y) { return y > kFp8Max ? kFp8Max : (y < -kFp8Max ? -kFp8Max : y); }
-
 // y / scale, rounded once to fp32: the product with the inverse can be a step off and lie on the other
 // side of a tie between two codes, so it is corrected by its remainder (with it, the 1.2 thousand million
 // quotients of every 24-bit divisor that are next to a tie of e4m3 all equal the division's).  Two
 // operations an element; the division's own sequence would take 5 to 14 % of the kernel's time.
 // Factors of 2 keep the inverse and the remainder in range.
 struct Divisor {
-  float m, s, inv;
+  float m, s, inv, most;
   __device__ __forceinline__ explicit Divisor(float scale) {
     const float mag = fabsf(scale);
     m = mag < 0x1p-70f ? 0x1p80f : mag > 0x1p100f ? 0x1p-64f : 1.0f;
     s = scale * m;
     inv = 1.0f / s;
+    most = kFp8Max * fabsf(s);
     if (isinf(s)) s = 0.0f;  // finite ones give zero, infinite ones NaN
-  }
-  // (y m) / (scale m).  BOUNDED: |y / scale| is no more than a step over 448, or not finite by the scale.
-  template <bool BOUNDED>
-  __device__ __forceinline__ float into(float y) const {
-    const float q = y * inv, r = __builtin_fmaf(q, s, -y), c = __builtin_fmaf(-r, inv, q);
-    if constexpr (BOUNDED) return c;
-    else return fabsf(q) < 1024.0f ? c : q;
   }
 };
 
-// The quotient clamped to the fp8 range.  By the row's own scale it is a step over 448 at most, which
-// the conversion rounds to 448.
+// The quotient y / (scale m), clamped to the fp8 range; NaN stays.  The clamp comes first, so that what is
+// divided is 448 scale at most, and the quotient a step over 448 at most, which the conversion rounds to 448.
+// By the row's own scale nothing is larger.
 template <bool ROW>
 __device__ __forceinline__ float quotient8(float y, const Divisor& d) {
-  if constexpr (ROW) return d.into<true>(y);
-  else return clamp8(d.into<false>(y));
+  if constexpr (!ROW) y = __builtin_elementwise_maximum(__builtin_elementwise_minimum(y, d.most), -d.most);
+  const float q = y * d.inv, r = __builtin_fmaf(q, d.s, -y);
+  return __builtin_fmaf(-r, d.inv, q);
 }
 
 // Larger of two magnitudes; NaN wins.

@@ -365,3 +365,18 @@ def test_gain_gradient_of_more_columns_than_a_grid_takes_at_once(lib):
     lib.rmsnorm_backward(dy, h, gain, rstd, dx, dgain)
     want = R.norm_grads(dy, h, gain, rstd)[1]
     near(dgain, want, (T + 16 + 4) * R.U * (dy.double().abs() * h.double().abs() * rstd.double()[:, None]).sum(0) + 2.0 ** -140)
+
+
+@pytest.mark.parametrize("D", [64, 4096, 3001, 32768])
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 2.0 ** -120, 2.0 ** 100, 3e38, float("inf"), float("nan")])
+def test_norm_unbounded_values_by_a_given_scale(lib, D, scale):
+    """Infinities and the largest numbers give 448, NaN and inf / inf NaN, under scales of every size."""
+    gain = torch.ones(D) * 3.0
+    gain[1:8] = torch.tensor([float("inf"), -float("inf"), float("nan"), 3.4e38, -3.4e38, 1e-45, 0.0])
+    s = torch.tensor([scale])
+    y = unit_rows(lib, gain, y_scale=s.cuda(), scale_mode="tensor")
+    want = (gain / s).clamp(-448, 448)
+    got = y[0].float()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert torch.equal(y[0].view(torch.uint8)[ok], want.to(FP8).view(torch.uint8)[ok])
