@@ -42,7 +42,8 @@ extern "C" {
  *   rstd             T fp32 or NULL.
  *   amax             one fp32 or NULL: raised to max |y| over the tensor where that is larger
  *                    (the caller sets it to 0 first; NaN sticks), for the next tensor scale.
- * D is any length >= 1; rows of D <= 16384 take one pass over memory, fastest where D % 8 == 0.  T D < 2^48 / 4.
+ * D is any length from 1 to 2^31 - 1, T below 2^31, every tensor below 2^48 bytes; rows of D <= 16384 take
+ * one pass over memory, fastest where D % 8 == 0.
  */
 forge_status forge_rmsnorm(const forge_tensor* x, const forge_tensor* residual, const forge_tensor* gain, float eps,
                            forge_tensor* h, forge_tensor* y, int32_t scale_mode, float* rstd, float* amax,
@@ -81,7 +82,8 @@ int64_t forge_rmsnorm_backward_workspace_bytes(int64_t T, int64_t D); /* -1 for 
  *                      elements at 2^-13 of the largest one's power of two before they add them.
  * forge_grouped_dgrad  dX[t] = dY[t] W_e, likewise (all BF16).
  * forge_grouped_wgrad  dW_e = dY_e^T X_e for every group, fp32 [n_groups * N, K] (zeros for an
- *                      empty group); X, dY BF16.
+ *                      empty group); X, dY BF16, each below 4 GiB with 128 rows more (here and in
+ *                      the step).
  * forge_grouped_wgrad_step  the same gradient, applied to every expert's weight by rule `opt` in
  *                      the product's epilogue as forge_wgrad_step does (an empty group takes the
  *                      step with a zero gradient); W BF16 with n_groups N K < 2^32, m, v as there.

@@ -9,10 +9,10 @@
 // XCDs in contiguous runs: an XCD's resident tiles share their weight and row panels in its L2
 // (16384 x 14336 x 4096: 79 % of the L2's requests hit).
 //
-// Measured: 16384 rows of 8 uneven experts by 14336 x 4096 in bf16 1.42-1.46 ms (1.32-1.35
-// PFLOP/s); in even groups 1.36 ms, where eight calls of the library, one an expert, take 1.42 and
+// Measured, over the cards seen: 16384 rows of 8 uneven experts by 14336 x 4096 in bf16 1.41-1.51 ms
+// (1.27-1.36 PFLOP/s); in even groups 1.36 ms, where eight calls of the library, one an expert, take 1.42 and
 // its product of one weight of that size 1.26.  16384 rows of 32 experts by 4096 x 4096 in fp8
-// 0.30-0.31 ms (1.8 PFLOP/s).  Input gradient of 32768 rows of 64 experts by 1408 x 2048 0.21 ms.
+// 0.29-0.33 ms (1.7-1.9 PFLOP/s).  Input gradient of 32768 rows of 64 experts by 1408 x 2048 0.20-0.22 ms.
 // The card's power bounds the bf16 product: the clock falls to 1.6-1.7 GHz while the matrix cores are
 // 85 % busy within a tile (74 % over the launch).  The others are at 41 % and 42 % and 2 GHz: shorter
 // contractions over more, ragged groups.  There it is what a workgroup alone on its CU cannot hide:
@@ -101,7 +101,7 @@ struct RowTile {
 // Up to this many tiles of 256 columns, the tiles take 128, all still on CUs at once: a product of
 // few rows is a pass over the live experts' weights, and wants many CUs to read.  Experts of 1024 x
 // 2048 in bf16: 30 live ones 29.3 us in 120 wide tiles, 26.0 us in 240 narrow ones (4.8 TB/s); 39 live
-// ones 38.5 us in 156 wide tiles, 50.9 us in 312 narrow ones.
+// ones 38.5 us in 156 wide tiles, 50.9 us in 312 narrow ones.  Contractions of other lengths were not compared.
 constexpr int NARROW_TILES = 128;
 
 // The tile of workgroup b among the row tiles of BM rows x the column tiles of O columns, of 256

@@ -29,8 +29,8 @@ namespace grp {
 // dW_e = dY_e^T X_e in fp32, 256 x 256 tiles of the contraction of forge_grouped.h (half as high or
 // wide at the end of an odd multiple of 128) over the group's rows alone: the operands' ranges begin
 // at the group's first row and end with its last, so a ragged end reads as zero.  32 experts of
-// 1408 x 2048, 16384 rows: 143 us (158 us where the stores displace the operands in L2), 3.4 TB/s;
-// a tile's stores come after its contraction, and nothing else runs on its CU.
+// 1408 x 2048, 16384 rows: 143-165 us over the cards seen, 2.9-3.4 TB/s (stores that displace the operands in L2: 158
+// us where these took 143); a tile's stores come after its contraction, and nothing else runs on its CU.
 template <int HEIGHT, int WIDTH>
 __device__ __forceinline__ void wgrad_tile_f32(const GroupedWgradArgs& a, float* dW, int e, int start, int len, int n0,
                                                int k0, unsigned char* smem) {

@@ -8,8 +8,9 @@
 // zero and an empty group contracts nothing.  Two workgroups share a CU: a tile is mostly epilogue
 // (20 bytes a weight with fp32 moments), and one workgroup's contraction runs beside the other's
 // epilogue; a 256 x 256 tile of one workgroup a CU would have nothing beside it.  8 experts of
-// 4096 x 4096, 8192 rows, AdamW with fp32 moments: 714 us, 3.9 TB/s of the 2.8 GB that it cannot do
-// without (594 us at a copy's 4.75 TB/s) and 385 TFLOP/s besides.  Experts follow each other in the launch, each
+// 4096 x 4096, 8192 rows, AdamW with fp32 moments: 645-727 us over the cards seen, 3.9-4.4 TB/s of the 2.8 GB that it
+// cannot do without (594 us at a copy's 4.75 TB/s) and 380-430 TFLOP/s besides; with 8-bit moments in the linear map 474
+// us, in the dynamic map, whose codes take many more operations, 1110 us.  Experts follow each other in the launch, each
 // spread over all XCDs, so that a crowded expert does not hold up one XCD.
 #pragma once
 

@@ -11,9 +11,9 @@
 // block of 64.  Elements past the last whole unit (n mod 4) or block (n mod 64) are updated by
 // one wave, a lane to an element.
 //
-// Measured: 120 tensors of 1000 .. 20 M elements in fp32 with bf16 gradients 1.24 ms, 40 of 4096 ..
-// 50 M in bf16 with 8-bit moments 0.45 ms, both 5.3 TB/s (a large copy: 4.75); 65 gains of 256 .. 5120
-// elements 4.4 us.  Chunks of 4096 elements keep every workgroup's loads in flight at once.
+// Measured, over the cards seen: 120 tensors of 1000 .. 20 M elements in fp32 with bf16 gradients 1.12-1.24 ms
+// (5.3-5.8 TB/s; a large copy: 4.75), 40 of 4096 .. 50 M in bf16 with 8-bit moments in the linear map 0.45 ms (5.3), in
+// the dynamic map, whose codes take many more operations, 1.0 ms; 65 gains of 256 .. 5120 elements 4.4 us.  Chunks of 4096 elements keep every workgroup's loads in flight at once.
 #include <hip/hip_runtime.h>
 
 #include "forge_device.h"

@@ -18,7 +18,6 @@ from ._layer_abi import _MultiInfo, _MultiTensor
 
 SCALE_MODE = {"row": 0, "tensor": 1}
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
-_SIZE = {F32: 4, BF16: 2, FP8_E4M3: 1}
 
 
 # The smallest calls (a norm of one token, a step of a model's gains) take less time on the device
