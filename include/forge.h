@@ -74,7 +74,9 @@ typedef enum forge_dtype {
   FORGE_I8_B64 = 3,   /* signed int8 moment, codes -127..127; `scale` -> rows*cols/64 fp32 block absmax */
   FORGE_U8_B64 = 4,   /* non-negative uint8 moment, codes 0..255; `scale` -> rows*cols/64 fp32 block absmax */
   FORGE_I8DYN_B64 = 5, /* signed moment in the dynamic 8-bit map (see below); `scale` as FORGE_I8_B64 */
-  FORGE_U8DYN_B64 = 6  /* non-negative moment in the dynamic 8-bit map; `scale` as FORGE_U8_B64 */
+  FORGE_U8DYN_B64 = 6, /* non-negative moment in the dynamic 8-bit map; `scale` as FORGE_U8_B64 */
+  FORGE_FP8_B128 = 7,  /* e4m3 codes in blocks of 128 columns (forge_ffn.h); `scale` -> one fp32 for each block */
+  FORGE_I8_B128 = 8    /* signed int8 codes, likewise */
 } forge_dtype;
 
 /* 8-bit moments (Technical Summary section 2 "Precision and Fidelity": int8 optimizer states in

@@ -55,7 +55,9 @@ forge_status forge_rmsnorm(const forge_tensor* x, const forge_tensor* residual, 
  *     dx = rstd * (a - u * mean(a * u)) + dh     (the gradient of x and of residual)
  *     dgain[d] = sum_t dy * u
  *   dy, dh, h, dx    [T, D], all F32 or all BF16; dh (the gradient arriving on h itself) may be
- *                    NULL.  dx may be dy or dh itself, else it overlaps no input.
+ *                    NULL.  dx may be dy or dh itself, else it overlaps no input.  h may instead be
+ *                    codes (FP8_B128 or I8_B128 of forge_ffn.h, scale [T, ceil(D / 128)]): the
+ *                    formula then takes what they stand for, beside the rstd of the h that was.
  *   rstd             T fp32, as forge_rmsnorm wrote it.
  *   dgain            [1, D] F32, overwritten; NULL where it is not needed.  The sum over rows has
  *                    a fixed order: the same inputs give the same bits.

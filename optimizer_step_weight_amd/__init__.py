@@ -14,6 +14,9 @@ Entry points (same names as the C ABI in include/forge.h, without the ``forge_``
 and, from layer.py (include/forge_layer.h):
     rmsnorm, rmsnorm_backward, grouped_gemm, grouped_dgrad, grouped_wgrad, grouped_wgrad_step,
     MultiStep
+and, from ffn.py (include/forge_ffn.h):
+    grouped_gated, gated_backward, grouped_gated_dgrad, block_quantize, block_dequantize,
+    block_quantize_weight, grouped_block_gemm
 """
 from __future__ import annotations
 
@@ -25,7 +28,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libforge.so")
 
 OPT = {"adamw": 0, "nadam": 1, "radam": 2, "lion": 3, "rmsprop": 4, "adagrad": 5, "sgd": 6, "sgd_momentum": 7}
-F32, BF16, FP8_E4M3, I8_B64, U8_B64, I8DYN_B64, U8DYN_B64 = 0, 1, 2, 3, 4, 5, 6
+F32, BF16, FP8_E4M3, I8_B64, U8_B64, I8DYN_B64, U8DYN_B64, FP8_B128, I8_B128 = 0, 1, 2, 3, 4, 5, 6, 7, 8
 STATUS = {0: "FORGE_OK", 1: "FORGE_ERR_ARG", 2: "FORGE_ERR_SHAPE", 3: "FORGE_ERR_DTYPE", 4: "FORGE_ERR_LAYOUT",
           5: "FORGE_ERR_ALIAS", 6: "FORGE_ERR_DEVICE", 7: "FORGE_ERR_LAUNCH"}
 SCALARS = ("decay", "l2", "c1", "c2", "c3", "b1", "omb1", "b2", "omb2", "eps", "lr", "rectified")
@@ -345,15 +348,23 @@ forge_status_string = status_string
 forge_last_error = last_error
 
 
-# include/forge_layer.h (imported on first use: the module needs torch)
+# include/forge_layer.h and forge_ffn.h (imported on first use: the modules need torch)
 _LAYER = ("rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace", "grouped_gemm", "grouped_dgrad", "grouped_wgrad",
           "grouped_wgrad_step", "MultiStep", "forge_rmsnorm", "forge_rmsnorm_backward", "forge_grouped_gemm",
           "forge_grouped_dgrad", "forge_grouped_wgrad", "forge_grouped_wgrad_step")
+_FFN = ("grouped_gated", "gated_backward", "grouped_gated_dgrad", "block_quantize", "block_dequantize",
+        "block_quantize_weight", "grouped_block_gemm", "forge_grouped_gated", "forge_gated_backward",
+        "forge_grouped_gated_dgrad", "forge_block_quantize", "forge_block_dequantize", "forge_block_quantize_weight",
+        "forge_grouped_block_gemm")
 
 
 def __getattr__(name: str):
     if name in _LAYER:
         from . import layer
         globals().update({n: getattr(layer, n) for n in _LAYER})
+        return globals()[name]
+    if name in _FFN:
+        from . import ffn
+        globals().update({n: getattr(ffn, n) for n in _FFN})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,4 +1,4 @@
-"""Structures and argument types of include/forge_layer.h.  Without torch: the library's host calls need none."""
+"""Structures and argument types of include/forge_layer.h and forge_ffn.h.  Without torch: the library's host calls need none."""
 from __future__ import annotations
 
 import ctypes
@@ -35,6 +35,16 @@ def declare(L) -> None:
     L.forge_multi_table_bytes.argtypes = [P(_MultiTensor), i32]
     L.forge_multi_pack.argtypes = [P(_MultiTensor), i32, i32, i32, i32, vp, i64, P(_MultiInfo)]
     L.forge_multi_step.argtypes = [P(_MultiInfo), vp, H, i32, i64, vp, O, vp]
+    L.forge_block_quantize.argtypes = [T, T, vp]
+    L.forge_block_dequantize.argtypes = [T, T, vp]
+    L.forge_block_quantize_weight.argtypes = [T, i32, T, T, vp]
+    L.forge_grouped_block_gemm.argtypes = [T, T, vp, i32, T, vp]
+    L.forge_grouped_gated.argtypes = [T, T, vp, i32, i32, T, T, vp]
+    L.forge_gated_backward.argtypes = [T, T, i32, T, T, vp]
+    L.forge_grouped_gated_dgrad.argtypes = [T, T, vp, i32, T, i32, T, T, vp]
+    for f in ("forge_block_quantize", "forge_block_dequantize", "forge_block_quantize_weight", "forge_grouped_block_gemm",
+              "forge_grouped_gated", "forge_gated_backward", "forge_grouped_gated_dgrad"):
+        getattr(L, f).restype = st
     for f in ("forge_rmsnorm", "forge_rmsnorm_backward", "forge_grouped_gemm", "forge_grouped_dgrad",
               "forge_grouped_wgrad", "forge_grouped_wgrad_step", "forge_multi_pack", "forge_multi_step"):
         getattr(L, f).restype = st

@@ -1,0 +1,96 @@
+// forge_ffn_internal.h -- structures shared by the entry points of forge_ffn.h and their kernels.
+#pragma once
+
+#include <stdint.h>
+
+#include "forge_layer_internal.h"
+
+namespace forge {
+
+// How an activation tensor is kept (FORGE_Q_FP8, FORGE_Q_I8: forge_layer_internal.h).
+enum : int { FORGE_KEEP_NONE = 0, FORGE_KEEP_BF16 = 1, FORGE_KEEP_FP8 = 2, FORGE_KEEP_I8 = 3, FORGE_KEEP_F32 = 4 };
+enum : int { FORGE_ACT_K_SILU = 0, FORGE_ACT_K_GELU = 1, FORGE_ACT_K_GELU_TANH = 2, FORGE_ACT_K_RELU = 3 };
+
+// Gate and up [T, 2 N]: blocks of the 8-bit forms begin at column 0 of either half.
+struct KeptArgs {
+  void* data;
+  float* scale;    // 8-bit: [T, 2, ceil(N / 128)]
+  int32_t type;    // FORGE_KEEP_*
+};
+
+// H = act(X Wg^T) * (X Wu^T), W [E, 2 N, K].
+struct GatedArgs {
+  const void* X;
+  const void* W;
+  const int32_t* ends;
+  uint16_t* H;     // [T, N] bf16
+  KeptArgs keep;   // written
+  int32_t E, act;
+  int32_t cols;    // least rows of W a tile takes: 256 or 128
+  int64_t T, N, K;
+};
+int launch_grouped_gated(const GatedArgs& a, void* stream);
+
+// dH = dY W, W [E, K, N]; from it and the kept gate and up d(gate, up) and H.
+struct GatedDgradArgs {
+  const void* dY;
+  const void* W;
+  const int32_t* ends;
+  KeptArgs keep;   // read
+  uint16_t* dGU;   // [T, 2 N] bf16
+  uint16_t* H;     // or null
+  int32_t E, act;
+  int32_t cols;
+  int64_t T, N, K;
+};
+int launch_grouped_gated_dgrad(const GatedDgradArgs& a, void* stream);
+
+// The same from dH itself; types F32 or BF16.
+struct GatedBwdArgs {
+  const void* dH;
+  KeptArgs keep;
+  void* dGU;
+  void* H;         // or null
+  int64_t T, N;
+  int32_t act, bf16;
+};
+int launch_gated_backward(const GatedBwdArgs& a, void* stream);
+
+// Codes of blocks of 1 x 128.
+struct BlockArgs {
+  const void* x;   // F32 or BF16 (quantise), codes (dequantise)
+  void* y;
+  float* scale;    // [T, ceil(D / 128)]
+  int64_t T, D;
+  int32_t bf16, q;
+};
+int launch_block_quantize(const BlockArgs& a, void* stream);
+int launch_block_dequantize(const BlockArgs& a, void* stream);
+
+// Codes of blocks of 128 x 128 of E weights [N, K], and their transposed copy.
+struct BlockWeightArgs {
+  const void* W;
+  uint8_t* q;      // [E, N, K]
+  float* scale;    // [E, N / 128, K / 128]
+  uint8_t* qt;     // [E, K, N] or null
+  float* scale_t;
+  int64_t E, N, K;
+  int32_t bf16;
+};
+int launch_block_quantize_weight(const BlockWeightArgs& a, void* stream);
+
+// Y_e = X_e W_e^T of codes with block scales.
+struct BlockGemmArgs {
+  const uint8_t* X;       // [T, K]
+  const uint8_t* W;       // [E, N, K]
+  const float* x_scale;   // [T, K / 128]
+  const float* w_scale;   // [E, N / 128, K / 128]
+  const int32_t* ends;
+  uint16_t* Y;            // [T, N] bf16
+  int32_t E;
+  int32_t cols;
+  int64_t T, N, K;
+};
+int launch_grouped_block_gemm(const BlockGemmArgs& a, void* stream);
+
+}  // namespace forge

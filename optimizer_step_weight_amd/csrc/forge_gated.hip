@@ -1,0 +1,124 @@
+// forge_gated.hip -- H = act(X Wg^T) * (X Wu^T) for the rows of every group, and gate and up as they are
+// kept for the backward pass, in one launch.
+//
+// A tile of forge_grouped.h takes 128 columns of H: its 256 rows of the stacked weight [2 N, K] are the 128
+// gate rows of these columns and their 128 up rows, which is all that the products know of the
+// activation.  The epilogue is in forge_gated.h.
+#include <hip/hip_runtime.h>
+
+#include "forge_gated.h"
+
+namespace forge {
+namespace grp {
+
+// The operand of S::WIDTH / 2 rows from `first` on and as many `gap` bytes after them.
+template <class S>
+__device__ __forceinline__ void open_pair(Feed<S>& f, const void* first, uint32_t gap, uint32_t ld, int slabs) {
+  constexpr int HALF = S::WIDTH / 2;
+  f.open(first, gap + HALF * ld, ld, slabs);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int j = 0; j < S::DMA; ++j) {
+    const int r = S::RPD * (S::DMA * wave + j) + lane / S::CPR;
+    if (r >= HALF) f.off[j] += gap - (uint32_t)HALF * ld;
+  }
+}
+
+// One row's 8 columns of H from gate and up; n: column of H.
+template <bool WIDE>
+__device__ __forceinline__ void gated_row(const GatedArgs& a, int64_t row, int64_t n, bool live, const float (&g)[8],
+                                          const float (&u)[8]) {
+  float h[8];
+  by_act(a.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v, s;
+      act_pair<decltype(act)::value>(g[i], v, s);
+      h[i] = v * u[i];
+    }
+  });
+  if (live) st16_stream(a.H + row * a.N + n, to_bf16x8(h));
+  if (a.keep.type == FORGE_KEEP_BF16) {
+    uint16_t* p = static_cast<uint16_t*>(a.keep.data) + row * 2 * a.N + n;
+    if (live) {
+      st16_stream(p, to_bf16x8(g));
+      st16_stream(p + a.N, to_bf16x8(u));
+    }
+  }
+  if constexpr (WIDE) {  // 16 lanes have a block's 128 columns
+    auto eight = [&](auto qc) {
+      constexpr int Q = decltype(qc)::value;
+      auto part = [&](const float (&v)[8], int64_t col, int64_t block) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = amax2(m, fabsf(v[i]));
+        const float scale = block_scale<Q>(max16(m));
+        if (!live) return;
+        store_codes<false>(static_cast<uint8_t*>(a.keep.data) + row * 2 * a.N + col, encode8<Q>(v, scale), 8);
+        if ((threadIdx.x & 15) == 0) a.keep.scale[row * (a.N / 64) + block] = scale;
+      };
+      part(g, n, n >> 7);
+      part(u, a.N + n, (a.N + n) >> 7);
+    };
+    if (a.keep.type == FORGE_KEEP_FP8) eight(std::integral_constant<int, FORGE_Q_FP8>{});
+    if (a.keep.type == FORGE_KEEP_I8) eight(std::integral_constant<int, FORGE_Q_I8>{});
+  }
+}
+
+template <int HEIGHT, int WIDTH>
+__device__ __forceinline__ void gated_tile(const GatedArgs& a, const RowTile& t, unsigned char* smem) {
+  using A = Side<2, false, 64 * HEIGHT>;
+  using B = Side<2, false, 64 * WIDTH>;
+  const int64_t n0 = (int64_t)t.n * (32 * WIDTH);  // column of H
+  const int slabs = t.e < a.E ? (int)(a.K / 64) : 0;
+  const uint32_t ld = (uint32_t)(a.K * 2);
+  Feed<A> fa;
+  Feed<B> fb;
+  fa.open(static_cast<const uint16_t*>(a.X) + (int64_t)t.row0 * a.K, (uint32_t)(t.rows * ld), ld, slabs);
+  open_pair(fb, static_cast<const uint16_t*>(a.W) + ((int64_t)t.e * 2 * a.N + n0) * a.K, (uint32_t)(a.N * ld), ld, slabs);
+  Tile<A, B> tile;
+  tile.contract(smem, fa, fb, slabs);
+  using R = Rounds<HEIGHT, WIDTH>;
+  constexpr int LANES = 4 * WIDTH;  // of a row
+  by_rounds<HEIGHT, WIDTH>(smem, tile, [&](int round) {
+    const int p = (int)threadIdx.x % LANES;
+    for (int r = (int)threadIdx.x / LANES; r < R::ROWS; r += THREADS / LANES) {
+      const int row = R::tile_row(round, r);
+      float g[8], u[8];
+      R::get(smem, r, 0, p, g);
+      R::get(smem, r, 8 * WIDTH, p, u);
+      gated_row<WIDTH == 4>(a, t.row0 + row, n0 + 8 * p, row < t.rows, g, u);
+    }
+  });
+}
+
+__global__ __launch_bounds__(THREADS, 1) void gated_kernel(GatedArgs a) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * 32768];
+  RowTile t;
+  if (!find_tile<256>(a.ends, a.E, a.T, 2 * a.N, a.cols, (int)blockIdx.x, t)) return;
+  switch ((t.rows + 63) / 64 + (t.cols < 256 ? 4 : 0)) {
+    case 1: gated_tile<1, 4>(a, t, smem); break;
+    case 2: gated_tile<2, 4>(a, t, smem); break;
+    case 3: gated_tile<3, 4>(a, t, smem); break;
+    case 4: gated_tile<4, 4>(a, t, smem); break;
+    case 5: gated_tile<1, 2>(a, t, smem); break;
+    case 6: gated_tile<2, 2>(a, t, smem); break;
+    case 7: gated_tile<3, 2>(a, t, smem); break;
+    case 8: gated_tile<4, 2>(a, t, smem); break;
+  }
+}
+
+}  // namespace grp
+
+int launch_grouped_gated(const GatedArgs& given, void* stream) {
+  GatedArgs a = given;
+  const int64_t O = 2 * a.N;
+  const int64_t row_tiles = a.T / 256 + (a.E < a.T ? a.E : a.T) + 1;
+  // as launch_grouped_rows; a narrow tile has half a block of 8-bit gate and up
+  a.cols = a.keep.type < FORGE_KEEP_FP8 && a.T / 256 * ((O + 255) / 256) <= grp::NARROW_TILES ? 128 : 256;
+  const int64_t tiles = row_tiles * ((O + a.cols - 1) / a.cols);
+  hipLaunchKernelGGL(grp::gated_kernel, dim3((unsigned)tiles), dim3(grp::THREADS), 0, (hipStream_t)stream, a);
+  return (int)hipGetLastError();
+}
+
+}  // namespace forge

@@ -44,7 +44,9 @@ int64_t dtype_size(int32_t dt) {
     case FORGE_I8_B64:
     case FORGE_U8_B64:
     case FORGE_I8DYN_B64:
-    case FORGE_U8DYN_B64: return 1;
+    case FORGE_U8DYN_B64:
+    case FORGE_FP8_B128:
+    case FORGE_I8_B128: return 1;
   }
   return 0;
 }

@@ -11,45 +11,12 @@
 #include "forge.h"
 #include "forge_host_common.h"
 #include "forge_layer.h"
+#include "forge_layer_host.h"
 #include "forge_layer_internal.h"
 
 using namespace forge::host;
 
 namespace {
-
-// Ranges of one call: written ones overlap nothing, except pairs named as allowed in place.
-struct Ranges {
-  Range r[16];
-  bool written[16];
-  int n = 0;
-  void add(const void* p, int64_t bytes, const char* name, bool w) {
-    r[n] = range_of(p, bytes, name);
-    written[n++] = w;
-  }
-  void add(const forge_tensor* t, const char* name, bool w) { add(t->data, bytes_of(t), name, w); }
-  // may: written range i may be exactly range j
-  template <class May>
-  forge_status check(May&& may) const {
-    for (int i = 0; i < n; ++i)
-      for (int j = 0; j < n; ++j) {
-        if (i == j || !written[i] || (written[j] && j < i)) continue;
-        if (!overlap(r[i], r[j])) continue;
-        if (r[i].lo == r[j].lo && r[i].hi == r[j].hi && may(r[i].name, r[j].name)) continue;
-        return fail(FORGE_ERR_ALIAS, "%s overlaps %s", r[i].name, r[j].name);
-      }
-    return FORGE_OK;
-  }
-};
-bool never(const char*, const char*) { return false; }
-
-bool is_stream(int32_t dt) { return dt == FORGE_F32 || dt == FORGE_BF16; }
-
-forge_status check_shape(const forge_tensor* t, int64_t rows, int64_t cols, const char* name) {
-  if (t->rows != rows || t->cols != cols)
-    return fail(FORGE_ERR_SHAPE, "%s is [%lld, %lld], expected [%lld, %lld]", name, (long long)t->rows,
-                (long long)t->cols, (long long)rows, (long long)cols);
-  return FORGE_OK;
-}
 
 forge_status check_gain(const forge_tensor* gain, int64_t D) {
   forge_status st;
@@ -163,14 +130,18 @@ forge_status forge_rmsnorm_backward(const forge_tensor* dy, const forge_tensor* 
   if ((st = check_shape(h, T, D, "h")) != FORGE_OK) return st;
   if ((st = check_shape(dx, T, D, "dx")) != FORGE_OK) return st;
   if (dh && (st = check_shape(dh, T, D, "dh")) != FORGE_OK) return st;
-  if (h->dtype != dy->dtype || dx->dtype != dy->dtype || (dh && dh->dtype != dy->dtype))
-    return fail(FORGE_ERR_DTYPE, "dy, dh, h and dx must have the same dtype");
+  const bool codes = h->dtype == FORGE_FP8_B128 || h->dtype == FORGE_I8_B128;
+  if ((h->dtype != dy->dtype && !codes) || dx->dtype != dy->dtype || (dh && dh->dtype != dy->dtype))
+    return fail(FORGE_ERR_DTYPE, "dy, dh, h and dx must have the same dtype (h may be codes of blocks of 128)");
+  if (codes && !h->scale) return fail(FORGE_ERR_ARG, "8-bit h needs h->scale");
+  if (codes && !aligned4(h->scale)) return fail(FORGE_ERR_LAYOUT, "h->scale is not 4-byte aligned");
   if (!rstd && T > 0) return fail(FORGE_ERR_ARG, "rstd is NULL");
   if (!aligned4(rstd)) return fail(FORGE_ERR_LAYOUT, "rstd is not 4-byte aligned");
   Ranges rs;
   rs.add(dy, "dy", false);
   if (dh) rs.add(dh, "dh", false);
   rs.add(h, "h", false);
+  if (codes) rs.add(h->scale, 4 * T * ((D + 127) / 128), "h scales", false);
   rs.add(gain, "gain", false);
   rs.add(rstd, 4 * T, "rstd", false);
   rs.add(dx, "dx", true);
@@ -197,6 +168,8 @@ forge_status forge_rmsnorm_backward(const forge_tensor* dy, const forge_tensor* 
   a.dy = dy->data;
   a.dh = dh ? dh->data : nullptr;
   a.h = h->data;
+  a.h_scale = codes ? static_cast<const float*>(h->scale) : nullptr;
+  a.h_q = !codes ? forge::FORGE_Q_NONE : h->dtype == FORGE_FP8_B128 ? forge::FORGE_Q_FP8 : forge::FORGE_Q_I8;
   a.gain = gain->data;
   a.rstd = rstd;
   a.dx = dx->data;
@@ -209,18 +182,6 @@ forge_status forge_rmsnorm_backward(const forge_tensor* dy, const forge_tensor* 
 }
 
 // ------------------------------------------------------------------ products grouped by expert
-static forge_status check_groups(const int32_t* ends, int32_t n_groups, int64_t T, int64_t N, int64_t K) {
-  if (n_groups < 1 || n_groups > 4096) return fail(FORGE_ERR_ARG, "n_groups must be 1 .. 4096 (got %d)", (int)n_groups);
-  if (!ends) return fail(FORGE_ERR_ARG, "ends is NULL");
-  if (!aligned4(ends)) return fail(FORGE_ERR_LAYOUT, "ends is not 4-byte aligned");
-  if (N < 128 || K < 128 || N % 128 || K % 128)
-    return fail(FORGE_ERR_SHAPE, "N = %lld and K = %lld must be positive multiples of 128", (long long)N, (long long)K);
-  if (N > (1 << 20) || K > (1 << 20) || N * K >= (int64_t(1) << 31))
-    return fail(FORGE_ERR_SHAPE, "N and K must be at most 2^20 and N * K below 2^31");
-  if (T >= (int64_t(1) << 31) - 256) return fail(FORGE_ERR_SHAPE, "T must be below 2^31 - 256");
-  return FORGE_OK;
-}
-
 // Y = A W^T (nn = false: A [T, K], O = N) or A W (nn = true: A [T, N], O = K) by group.
 static forge_status grouped_rows(const forge_tensor* A, const forge_tensor* W, const int32_t* ends, int32_t n_groups,
                                  forge_tensor* out, bool nn, void* stream) {

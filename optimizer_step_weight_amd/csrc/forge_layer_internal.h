@@ -27,10 +27,15 @@ struct NormArgs {
 };
 int launch_rmsnorm(int x_bf16, int y_type, const NormArgs& a, void* stream);
 
+// 8-bit codes of blocks of 128 columns (forge_rows.h).
+enum : int { FORGE_Q_NONE = 0, FORGE_Q_FP8 = 1, FORGE_Q_I8 = 2 };
+
 struct NormBwdArgs {
   const void* dy;
   const void* dh;    // or null
-  const void* h;
+  const void* h;     // the type of dy, or 8-bit codes
+  const float* h_scale;  // 8-bit: [T, ceil(D / 128)]
+  int32_t h_q;
   const void* gain;
   const float* rstd;
   void* dx;

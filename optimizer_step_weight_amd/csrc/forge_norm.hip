@@ -19,137 +19,11 @@
 
 #include "forge_device.h"
 #include "forge_layer_internal.h"
+#include "forge_norm_backward.h"
 
 namespace forge {
 
 namespace {
-
-constexpr float kFp8Max = 448.0f;
-constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: keeps 1 / scale finite
-
-// 8 consecutive elements as loaded.
-template <bool BF>
-struct Raw8 {
-  u32x4 q[BF ? 1 : 2];
-};
-template <bool BF>
-__device__ __forceinline__ Raw8<BF> load8(const void* p, int64_t i) {
-  Raw8<BF> r;
-  if constexpr (BF) {
-    r.q[0] = ld16(static_cast<const uint16_t*>(p) + i);
-  } else {
-    r.q[0] = ld16(static_cast<const float*>(p) + i);
-    r.q[1] = ld16(static_cast<const float*>(p) + i + 4);
-  }
-  return r;
-}
-template <bool BF>
-__device__ __forceinline__ void unpack8(const Raw8<BF>& r, float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (BF) v[j] = (j & 1) ? __uint_as_float(r.q[0][j >> 1] & 0xFFFF0000u) : __uint_as_float(r.q[0][j >> 1] << 16);
-    else v[j] = __uint_as_float(r.q[j >> 2][j & 3]);
-  }
-}
-template <bool BF>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
-  if constexpr (BF) {
-    u32x4 q;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = f32_to_bf16_rne(v[2 * j]) | (f32_to_bf16_rne(v[2 * j + 1]) << 16);
-    __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i));
-  } else {
-    u32x4 a, b;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = __float_as_uint(v[j]);
-      b[j] = __float_as_uint(v[4 + j]);
-    }
-    st16(static_cast<float*>(p) + i, a);
-    st16(static_cast<float*>(p) + i + 4, b);
-  }
-}
-// The same from any alignment, and n < 8 elements one by one (the others are 0): rows whose bytes are
-// no multiple of 16.
-typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
-template <bool BF>
-__device__ __forceinline__ Raw8<BF> load_any(const void* p, int64_t i, int n) {
-  Raw8<BF> r;
-  const int64_t at = i * (BF ? 2 : 4);
-  const char* b = static_cast<const char*>(p) + at;
-  if (n == 8) {
-    r.q[0] = *reinterpret_cast<const u32x4u*>(b);
-    if constexpr (!BF) r.q[1] = *reinterpret_cast<const u32x4u*>(b + 16);
-    return r;
-  }
-  uint32_t v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = j >= n ? 0u : BF ? (uint32_t)reinterpret_cast<const uint16_t*>(b)[j] : reinterpret_cast<const uint32_t*>(b)[j];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (BF) r.q[0][j] = v[2 * j] | (v[2 * j + 1] << 16);
-    else {
-      r.q[0][j] = v[j];
-      r.q[1][j] = v[4 + j];
-    }
-  }
-  return r;
-}
-template <bool BF>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (BF) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  else return static_cast<const float*>(p)[i];
-}
-template <bool BF>
-__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-  if constexpr (BF) static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_rne(v);
-  else static_cast<float*>(p)[i] = v;
-}
-__device__ __forceinline__ float gain1(const void* p, int bf, int64_t i) {
-  return bf ? load1<true>(p, i) : load1<false>(p, i);
-}
-template <bool BF>
-__device__ __forceinline__ float round_to(float v) {
-  if constexpr (BF) return bf16_to_f32(f32_to_bf16_rne(v));
-  else return v;
-}
-
-template <bool BF>
-__device__ __forceinline__ void store_any(void* p, int64_t i, const float (&v)[8], int n) {
-  char* b = static_cast<char*>(p) + i * (BF ? 2 : 4);
-  if (n == 8) {
-    u32x4 q[BF ? 1 : 2];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (BF) q[0][j] = f32_to_bf16_rne(v[2 * j]) | (f32_to_bf16_rne(v[2 * j + 1]) << 16);
-      else {
-        q[0][j] = __float_as_uint(v[j]);
-        q[1][j] = __float_as_uint(v[4 + j]);
-      }
-    }
-    *reinterpret_cast<u32x4u*>(b) = q[0];
-    if constexpr (!BF) *reinterpret_cast<u32x4u*>(b + 16) = q[1];
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) store1<BF>(b, j, v[j]);
-}
-
-// A thread's 8 columns of a row, n of them in the row (ODD: the row's bytes are no multiple of 16).
-template <bool BF, bool ODD>
-__device__ __forceinline__ Raw8<BF> load_cols(const void* p, int64_t i, int n) {
-  if constexpr (ODD) return load_any<BF>(p, i, n);
-  else return load8<BF>(p, i);
-}
-template <bool BF, bool ODD>
-__device__ __forceinline__ void store_cols(void* p, int64_t i, const float (&v)[8], int n) {
-  if constexpr (ODD) store_any<BF>(p, i, v, n);
-  else store8<BF>(p, i, v);
-}
-__device__ __forceinline__ int cols_in(int c, int D) { return D - c < 0 ? 0 : D - c > 8 ? 8 : D - c; }
 
 // y / scale, rounded once to fp32: the product with the inverse can be a step off and lie on the other
 // side of a tie between two codes, so it is corrected by its remainder (with it, the 1.2 thousand million
@@ -176,32 +50,6 @@ __device__ __forceinline__ float quotient8(float y, const Divisor& d) {
   if constexpr (!ROW) y = __builtin_elementwise_maximum(__builtin_elementwise_minimum(y, d.most), -d.most);
   const float q = y * d.inv, r = __builtin_fmaf(q, d.s, -y);
   return __builtin_fmaf(-r, d.inv, q);
-}
-
-// Larger of two magnitudes; NaN wins.
-__device__ __forceinline__ float amax2(float a, float b) { return (a > b || a != a) ? a : b; }
-
-struct Sum {
-  static __device__ __forceinline__ float join(float a, float b) { return a + b; }
-};
-struct Max {
-  static __device__ __forceinline__ float join(float a, float b) { return amax2(a, b); }
-};
-
-// Reduction over the TPR threads of a row; red: TPR / 64 floats of this use (TPR > 64).
-template <class Op, int TPR>
-__device__ __forceinline__ float row_reduce(float v, float* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = Op::join(v, __shfl_xor(v, o));
-  if constexpr (TPR > 64) {
-    constexpr int NW = TPR / 64;
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v = Op::join(v, red[w]);
-  }
-  return v;
 }
 
 // Raises *amax to v (both non-negative or NaN: the bits order as unsigned integers, NaN above
@@ -371,117 +219,6 @@ __global__ __launch_bounds__(256) void rmsnorm_loop_kernel(NormArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ backward
-// Row group u (TPR threads) takes rows u T / G .. (u + 1) T / G - 1 and writes their share of
-// dgain to row u of the partial sums; dgain_kernel adds the rows in order.
-template <bool BF, bool DH, bool DG, bool ODD, int TPR, int NV>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_bwd_kernel(NormBwdArgs a, int64_t groups) {
-  constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR;
-  __shared__ float red[2][16];
-  const int lane = (int)threadIdx.x % TPR, sub = (int)threadIdx.x / TPR;
-  const int64_t u = (int64_t)blockIdx.x * RPB + sub;
-  if (u >= groups) return;
-  int64_t row = u * a.T / groups;
-  const int64_t end = (u + 1) * a.T / groups;
-  constexpr bool AHEAD = NV == 1;  // next row's loads in flight, gain in registers
-  int in[NV];
-  float gain[NV][8], acc[DG ? NV : 1][8];
-  auto fetch_gain = [&](int i) {
-    const int c = (lane + i * TPR) * 8;
-    if (a.gain_bf16) unpack8<true>(load_cols<true, ODD>(a.gain, c, in[i]), gain[i]);
-    else unpack8<false>(load_cols<false, ODD>(a.gain, c, in[i]), gain[i]);
-  };
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    in[i] = cols_in((lane + i * TPR) * 8, a.D);
-    if constexpr (DG)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-    if (AHEAD && in[i]) fetch_gain(i);
-  }
-  Raw8<BF> rdy[NV], rh[NV], rdh[DH ? NV : 1];
-  float rs = 0.0f;
-  auto fetch = [&](int64_t t) {
-    rs = a.rstd[t];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!in[i]) continue;
-      const int64_t at = t * a.D + (lane + i * TPR) * 8;
-      rdy[i] = load_cols<BF, ODD>(a.dy, at, in[i]);
-      rh[i] = load_cols<BF, ODD>(a.h, at, in[i]);
-      if constexpr (DH && AHEAD) rdh[i] = load_cols<BF, ODD>(a.dh, at, in[i]);
-    }
-  };
-  if (AHEAD && row < end) fetch(row);
-  const float inv_d = 1.0f / (float)a.D;
-  for (int par = 0; row < end; ++row, par ^= 1) {
-    if (!AHEAD) fetch(row);
-    float dy[NV][8], h[NV][8], dh[DH ? NV : 1][8], c = 0.0f;
-    const float s = rs;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!in[i]) continue;
-      unpack8<BF>(rdy[i], dy[i]);
-      unpack8<BF>(rh[i], h[i]);
-      if constexpr (DH && AHEAD) unpack8<BF>(rdh[i], dh[i]);
-      if (!AHEAD) fetch_gain(i);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[i][j] *= s;
-        c = __builtin_fmaf(dy[i][j] * gain[i][j], h[i][j], c);
-      }
-    }
-    if (AHEAD && row + 1 < end) fetch(row + 1);
-    c = row_reduce<Sum, TPR>(c, red[par]);
-    c *= inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!in[i]) continue;
-      if (!AHEAD) {
-        fetch_gain(i);
-        if constexpr (DH) unpack8<BF>(load_cols<BF, ODD>(a.dh, row * a.D + (lane + i * TPR) * 8, in[i]), dh[i]);
-      }
-      float dx[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dx[j] = s * __builtin_fmaf(-h[i][j], c, dy[i][j] * gain[i][j]);
-        if constexpr (DH) dx[j] += dh[i][j];
-        if constexpr (DG) acc[i][j] = __builtin_fmaf(dy[i][j], h[i][j], acc[i][j]);
-      }
-      store_cols<BF, ODD>(a.dx, row * a.D + (lane + i * TPR) * 8, dx, in[i]);
-    }
-  }
-  if constexpr (DG)
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (in[i]) store_cols<false, ODD>(a.partial, u * a.D + (lane + i * TPR) * 8, acc[i], in[i]);
-}
-
-template <bool BF>
-__global__ __launch_bounds__(256) void rmsnorm_bwd_loop_kernel(NormBwdArgs a, int64_t groups) {
-  __shared__ float red[2][16];
-  const int64_t u = blockIdx.x, first = u * a.T / groups, end = (u + 1) * a.T / groups;
-  float* part = a.partial + u * a.D;
-  if (a.dgain)
-    for (int64_t c = threadIdx.x; c < a.D; c += 256) part[c] = 0.0f;
-  int par = 0;
-  for (int64_t row = first; row < end; ++row, par ^= 1) {
-    const int64_t base = row * a.D;
-    const float s = a.rstd[row];
-    float sum = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.D; c += 256)
-      sum = __builtin_fmaf(load1<BF>(a.dy, base + c) * gain1(a.gain, a.gain_bf16, c), load1<BF>(a.h, base + c) * s, sum);
-    const float mean = row_reduce<Sum, 256>(sum, red[par]) * (1.0f / (float)a.D);
-    for (int64_t c = threadIdx.x; c < a.D; c += 256) {
-      const float dy = load1<BF>(a.dy, base + c), u = load1<BF>(a.h, base + c) * s;
-      float dx = s * __builtin_fmaf(-u, mean, dy * gain1(a.gain, a.gain_bf16, c));
-      if (a.dh) dx += load1<BF>(a.dh, base + c);
-      store1<BF>(a.dx, base + c, dx);
-      if (a.dgain) part[c] = __builtin_fmaf(dy, u, part[c]);
-    }
-  }
-}
-
 // dgain[c] = sum over the groups' partial rows, in a fixed order: thread (x, y) of 32 x 16 adds
 // rows y, y + 16, ..., then the 16 sums are added in order.  A workgroup takes 32 columns, and further
 // ones where D has more than a grid may (2^32 threads).
@@ -520,7 +257,6 @@ void by_width(int D, F&& f) {
   else if (D <= 8192) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
   else f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
 }
-bool in_registers(int D) { return D <= 16384; }
 
 template <bool BF, int YT>
 void forward(const NormArgs& a, hipStream_t st) {
@@ -536,29 +272,6 @@ void forward(const NormArgs& a, hipStream_t st) {
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(THREADS), 0, st, a); };
     if (a.D % 8) launch(a.res ? rmsnorm_kernel<BF, true, true, YT, TPR, NV> : rmsnorm_kernel<BF, false, true, YT, TPR, NV>);
     else launch(a.res ? rmsnorm_kernel<BF, true, false, YT, TPR, NV> : rmsnorm_kernel<BF, false, false, YT, TPR, NV>);
-  });
-}
-
-// The backward pass holds three rows and the gain's sums besides the gain: one vector a thread
-// keeps it at 5 waves a SIMD; two (1024 threads, 128 registers) fit without the next row's
-// loads in flight and the gain in registers.
-template <class F>
-void by_width_backward(int D, F&& f) {
-  using std::integral_constant;
-  if (D <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (D <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  else if (D <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
-  else if (D <= 8192) f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
-  else f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-}
-
-template <bool BF, bool DH, bool DG>
-void backward(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
-  by_width_backward(a.D, [&](auto tpr, auto nv) {
-    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr int RPB = TPR >= 256 ? 1 : 256 / TPR, THREADS = TPR > 256 ? TPR : 256;
-    hipLaunchKernelGGL((a.D % 8 ? rmsnorm_bwd_kernel<BF, DH, DG, true, TPR, NV> : rmsnorm_bwd_kernel<BF, DH, DG, false, TPR, NV>),
-                       dim3((unsigned)((groups + RPB - 1) / RPB)), dim3(THREADS), 0, st, a, groups);
   });
 }
 
@@ -583,21 +296,8 @@ int launch_rmsnorm(int x_bf16, int y_type, const NormArgs& a, void* stream) {
 int launch_rmsnorm_backward(int bf16, const NormBwdArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   const int64_t groups = norm_bwd_groups(a.T);
-  if (!in_registers(a.D)) {
-    if (bf16) hipLaunchKernelGGL(rmsnorm_bwd_loop_kernel<true>, dim3((unsigned)groups), dim3(256), 0, st, a, groups);
-    else hipLaunchKernelGGL(rmsnorm_bwd_loop_kernel<false>, dim3((unsigned)groups), dim3(256), 0, st, a, groups);
-  } else {
-    switch ((bf16 ? 4 : 0) + (a.dh ? 2 : 0) + (a.dgain ? 1 : 0)) {
-      case 0: backward<false, false, false>(a, groups, st); break;
-      case 1: backward<false, false, true>(a, groups, st); break;
-      case 2: backward<false, true, false>(a, groups, st); break;
-      case 3: backward<false, true, true>(a, groups, st); break;
-      case 4: backward<true, false, false>(a, groups, st); break;
-      case 5: backward<true, false, true>(a, groups, st); break;
-      case 6: backward<true, true, false>(a, groups, st); break;
-      case 7: backward<true, true, true>(a, groups, st); break;
-    }
-  }
+  if (a.h_q != FORGE_Q_NONE) launch_rmsnorm_backward_q8(bf16, a, groups, stream);
+  else backward_by_flags<FORGE_Q_NONE>(bf16, a, groups, st);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || !a.dgain) return (int)err;
   const int64_t blocks = ((int64_t)a.D + 31) / 32;

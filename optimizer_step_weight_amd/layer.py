@@ -107,12 +107,17 @@ def rmsnorm_backward_workspace(rows: int, width: int, device="cuda", *, stream=N
     return _workspace(n // 4, torch.float32, device, stream)
 
 
-def rmsnorm_backward(dy, h, gain, rstd, dx, dgain=None, *, dh=None, workspace=None, stream=None) -> None:
+def rmsnorm_backward(dy, h, gain, rstd, dx, dgain=None, *, dh=None, h_scale=None, workspace=None, stream=None) -> None:
     """dx (of x and of residual; dh, the gradient arriving on h itself, is added) and dgain
-    (float32, overwritten) of rmsnorm (forge_rmsnorm_backward).  A workspace is allocated, for the
-    stream of the call, where dgain is wanted and none is given."""
+    (float32, overwritten) of rmsnorm (forge_rmsnorm_backward).  h may be 8-bit codes (float8_e4m3fn or int8)
+    with h_scale, one for each 128 columns of a row, as block_quantize gives them.  A workspace is
+    allocated, for the stream of the call, where dgain is wanted and none is given."""
     dev = _device(h, "h")
-    H = _mat(h, "h", dev)
+    if h_scale is None:
+        H = _mat(h, "h", dev)
+    else:
+        from .ffn import _codes
+        H = _codes(h, "h", dev, h_scale)
     rows, width = H.rows, H.cols
     if dgain is not None and workspace is None:
         workspace = rmsnorm_backward_workspace(rows, width, h.device, stream=stream)

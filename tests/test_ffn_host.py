@@ -1,0 +1,180 @@
+"""Host side of include/forge_ffn.h, no GPU needed: refusals with their statuses (fake, never-dereferenced
+addresses), the binding's own checks, and the gated formulas against differences in 64 bits."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from tests import ffn_ref as R
+
+
+@pytest.fixture(scope="module")
+def f():
+    import optimizer_step_weight_amd as forge
+    if not os.path.exists(forge.LIB_PATH):
+        from optimizer_step_weight_amd import _build
+        _build.build(verbose=False)
+    forge._lib()
+    return forge
+
+
+FAKE, GB = 0x7F0000000000, 1 << 30
+ARG, SHAPE, DTYPE, LAYOUT, ALIAS = 1, 2, 3, 4, 5
+r = ctypes.byref
+
+
+def t(f, slot, rows, cols, dtype=None, off=0, scale=None, ld=None):
+    return f.Tensor(FAKE + slot * GB + off, f.BF16 if dtype is None else dtype, rows, cols, cols if ld is None else ld,
+                    scale)
+
+
+def ref(x):
+    return None if x is None else r(x)
+
+
+def test_codes_refusals(f):
+    L, T, D, S = f._lib(), 5, 300, FAKE + 9 * GB
+    q = lambda dt=f.FP8_B128, scale=S, rows=T, cols=D, **k: t(f, 1, rows, cols, dt, scale=scale, **k)  # noqa: E731
+    for call in (lambda x, c: L.forge_block_quantize(ref(x), ref(c), None), lambda x, c: L.forge_block_dequantize(ref(c), ref(x), None)):
+        for x, c, want in [
+            (None, q(), ARG), (t(f, 0, T, D), None, ARG), (t(f, 0, T, D, f.FP8_E4M3), q(), DTYPE), (t(f, 0, T, D), q(f.FP8_E4M3), DTYPE),
+            (t(f, 0, T, D), q(f.I8_B64), DTYPE), (t(f, 0, T, D), q(cols=D + 1), SHAPE), (t(f, 0, T, D), q(scale=None), ARG),
+            (t(f, 0, T, D), q(scale=S + 2), LAYOUT), (t(f, 0, T, D, off=8), q(), LAYOUT), (t(f, 0, T, D, ld=D + 8), q(), LAYOUT),
+            (t(f, 1, T, D), q(), ALIAS), (t(f, 0, T, 0), q(cols=0), SHAPE),
+        ]:
+            assert call(x, c) == want, f.last_error()
+        assert call(t(f, 0, 0, D), q(rows=0, scale=None)) == 0
+    assert L.forge_block_quantize(r(t(f, 0, T, D)), r(q(scale=FAKE + 1 * GB + 16)), None) == ALIAS
+    assert L.forge_block_quantize(r(t(f, 0, T, D)), r(q(scale=FAKE + 16)), None) == ALIAS
+
+
+def test_weight_codes_refusals(f):
+    L, E, N, K = f._lib(), 2, 256, 384
+    S, S2 = FAKE + 8 * GB, FAKE + 9 * GB
+    W, q, qt = t(f, 0, E * N, K), t(f, 1, E * N, K, f.FP8_B128, scale=S), t(f, 2, E * K, N, f.FP8_B128, scale=S2)
+    call = lambda w=W, e=E, a=q, b=qt: L.forge_block_quantize_weight(ref(w), e, ref(a), ref(b), None)  # noqa: E731
+    for kw, want in [
+        (dict(w=None), ARG), (dict(a=None), ARG), (dict(e=0), ARG), (dict(e=3), SHAPE), (dict(w=t(f, 0, E * N, 200)), SHAPE),
+        (dict(w=t(f, 0, E * N, K, f.FP8_E4M3)), DTYPE), (dict(a=t(f, 1, E * N, K, f.I8_B128, scale=S)), DTYPE),
+        (dict(b=t(f, 2, E * N, K, f.FP8_B128, scale=S2)), SHAPE), (dict(a=t(f, 1, E * N, K, f.FP8_B128)), ARG),
+        (dict(b=t(f, 2, E * K, N, f.FP8_B128)), ARG), (dict(b=t(f, 1, E * K, N, f.FP8_B128, scale=S2)), ALIAS),
+        (dict(b=t(f, 2, E * K, N, f.FP8_B128, scale=S)), ALIAS), (dict(a=t(f, 0, E * N, K, f.FP8_B128, scale=S)), ALIAS),
+    ]:
+        assert call(**kw) == want, (kw, f.last_error())
+
+
+def test_block_product_refusals(f):
+    L, T, N, K, E = f._lib(), 70, 256, 384, 3
+    S, S2, ends = FAKE + 8 * GB, FAKE + 9 * GB, FAKE + 6 * GB
+    X, W, Y = t(f, 0, T, K, f.FP8_B128, scale=S), t(f, 1, E * N, K, f.FP8_B128, scale=S2), t(f, 2, T, N)
+    call = lambda x=X, w=W, at=ends, n=E, y=Y: L.forge_grouped_block_gemm(ref(x), ref(w), at, n, ref(y), None)  # noqa: E731
+    for kw, want in [
+        (dict(x=None), ARG), (dict(w=None), ARG), (dict(y=None), ARG), (dict(at=None), ARG), (dict(n=0), ARG), (dict(at=ends + 1), LAYOUT),
+        (dict(n=2), SHAPE), (dict(x=t(f, 0, T, K, f.FP8_E4M3, scale=S)), DTYPE), (dict(w=t(f, 1, E * N, K, f.I8_B128, scale=S2)), DTYPE),
+        (dict(y=t(f, 2, T, N, f.F32)), DTYPE), (dict(x=t(f, 0, T, K, f.FP8_B128)), ARG), (dict(w=t(f, 1, E * N, K, f.FP8_B128)), ARG),
+        (dict(x=t(f, 0, T, 200, f.FP8_B128, scale=S), w=t(f, 1, E * N, 200, f.FP8_B128, scale=S2)), SHAPE),
+        (dict(y=t(f, 0, T, N)), ALIAS), (dict(x=t(f, 0, T, K, f.FP8_B128, scale=FAKE + 2 * GB)), ALIAS), (dict(at=FAKE + 2 * GB), ALIAS),
+    ]:
+        assert call(**kw) == want, (kw, f.last_error())
+    assert call(x=t(f, 0, 0, K, f.FP8_B128), y=t(f, 2, 0, N)) == 0
+
+
+def test_gated_refusals(f):
+    L, T, N, K, E = f._lib(), 70, 256, 384, 3
+    ends, S = FAKE + 6 * GB, FAKE + 9 * GB
+    X, W, H = t(f, 0, T, K), t(f, 1, E * 2 * N, K), t(f, 2, T, N)
+    G = t(f, 3, T, 2 * N, f.I8_B128, scale=S)
+    call = lambda x=X, w=W, at=ends, n=E, act=0, h=H, g=G: L.forge_grouped_gated(ref(x), ref(w), at, n, act, ref(h), ref(g), None)  # noqa: E731
+    for kw, want in [
+        (dict(x=None), ARG), (dict(w=None), ARG), (dict(h=None), ARG), (dict(at=None), ARG), (dict(n=4097), ARG), (dict(act=4), ARG),
+        (dict(act=-1), ARG), (dict(w=t(f, 1, E * N, K)), SHAPE), (dict(h=t(f, 2, T, N + 64)), SHAPE), (dict(h=t(f, 2, T + 1, N)), SHAPE),
+        (dict(x=t(f, 0, T, K, f.F32)), DTYPE), (dict(h=t(f, 2, T, N, f.F32)), DTYPE), (dict(g=t(f, 3, T, N)), SHAPE),
+        (dict(g=t(f, 3, T, 2 * N, f.F32)), DTYPE), (dict(g=t(f, 3, T, 2 * N, f.I8_B64, scale=S)), DTYPE),
+        (dict(g=t(f, 3, T, 2 * N, f.FP8_B128)), ARG), (dict(g=t(f, 2, T, 2 * N)), ALIAS), (dict(h=t(f, 0, T, N)), ALIAS),
+        (dict(g=t(f, 3, T, 2 * N, f.FP8_B128, scale=FAKE + 2 * GB)), ALIAS),
+        (dict(x=t(f, 0, T, 1 << 20), w=t(f, 1, E * 2048, 1 << 20), h=t(f, 2, T, 1024), g=None), SHAPE),
+    ]:
+        assert call(**kw) == want, (kw, f.last_error())
+    assert call(x=t(f, 0, 0, K), h=t(f, 2, 0, N), g=None) == 0
+
+
+def test_gated_backward_refusals(f):
+    L, T, N, K, E = f._lib(), 70, 256, 384, 3
+    ends, S = FAKE + 6 * GB, FAKE + 9 * GB
+    G, d, H = t(f, 1, T, 2 * N, f.FP8_B128, scale=S), t(f, 2, T, 2 * N), t(f, 3, T, N)
+    call = lambda x=t(f, 0, T, N), g=G, act=0, d=d, h=H: L.forge_gated_backward(ref(x), ref(g), act, ref(d), ref(h), None)  # noqa: E731
+    both = [
+        (dict(g=None), ARG), (dict(d=None), ARG), (dict(act=9), ARG), (dict(g=t(f, 1, T, N)), SHAPE), (dict(d=t(f, 2, T, N)), SHAPE),
+        (dict(h=t(f, 3, T, N + 1)), SHAPE), (dict(g=t(f, 1, T, 2 * N, f.F32)), DTYPE), (dict(d=t(f, 2, T, 2 * N, f.F32)), DTYPE),
+        (dict(h=t(f, 3, T, N, f.F32)), DTYPE), (dict(g=t(f, 1, T, 2 * N, f.I8_B128)), ARG), (dict(d=t(f, 1, T, 2 * N)), ALIAS),
+        (dict(h=t(f, 2, T, N)), ALIAS), (dict(g=t(f, 1, T, 2 * N, f.I8_B128, scale=FAKE + 2 * GB)), ALIAS),
+        (dict(g=t(f, 2, T, 2 * N), d=t(f, 2, T, 2 * N, off=32)), ALIAS),
+    ]
+    for kw, want in both + [(dict(x=None), ARG), (dict(x=t(f, 0, T, N, f.I8_B128)), DTYPE), (dict(d=t(f, 0, T, 2 * N)), ALIAS)]:
+        assert call(**kw) == want, (kw, f.last_error())
+    z = lambda s, c, dt=None: t(f, s, 0, c, dt)  # noqa: E731
+    assert call(x=z(0, N), g=z(1, 2 * N), d=z(1, 2 * N), h=z(0, N)) == 0 and call(x=z(0, N), g=z(1, 2 * N, f.I8_B128), d=z(2, 2 * N), h=None) == 0
+    W = t(f, 4, E * K, N)
+    call = lambda x=t(f, 0, T, K), w=W, at=ends, n=E, g=G, act=0, d=d, h=H: L.forge_grouped_gated_dgrad(  # noqa: E731
+        ref(x), ref(w), at, n, ref(g), act, ref(d), ref(h), None)
+    for kw, want in both + [(dict(x=None), ARG), (dict(w=None), ARG), (dict(at=None), ARG), (dict(w=t(f, 4, E * N, K)), SHAPE),
+                            (dict(x=t(f, 0, T, K, f.F32)), DTYPE), (dict(w=t(f, 4, E * K, N, f.FP8_E4M3)), DTYPE),
+                            (dict(h=t(f, 4, T, N)), ALIAS), (dict(d=t(f, 0, T, 2 * N)), ALIAS)]:
+        assert call(**kw) == want, (kw, f.last_error())
+    assert call(x=z(0, K), g=z(1, 2 * N), d=z(2, 2 * N), h=None) == 0
+
+
+def test_norm_backward_of_codes_refusals(f):
+    T, D, S = 5, 384, FAKE + 9 * GB
+    L = f._lib()
+
+    def call(h, dx=t(f, 5, T, D)):
+        return L.forge_rmsnorm_backward(r(t(f, 0, T, D)), None, r(h), r(t(f, 3, 1, D, f.F32)), FAKE + 4 * GB, r(dx), None, None, 0, None)
+    assert call(t(f, 2, T, D, f.I8_B128)) == ARG and call(t(f, 2, T, D, f.FP8_B128, scale=S + 1)) == LAYOUT
+    assert call(t(f, 2, T, D, f.FP8_E4M3, scale=S)) == DTYPE and call(t(f, 2, T, D, f.I8_B64, scale=S)) == DTYPE
+    assert call(t(f, 2, T, D, f.I8_B128, scale=FAKE + 5 * GB)) == ALIAS and call(t(f, 5, T, D, f.I8_B128, scale=S)) == ALIAS
+
+
+def test_binding_checks_before_the_library(f):
+    """CPU tensors, and arguments that go together, raise in the binding."""
+    x, q, s = torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(2, 256, dtype=torch.int8), torch.zeros(2, 2)
+    w = torch.zeros(1, 256, 256, dtype=torch.bfloat16)
+    ends = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: f.block_quantize(x, q, s), lambda: f.block_dequantize(q, s, x),
+                 lambda: f.block_quantize_weight(w, q, s), lambda: f.grouped_gated(x, w, ends, x),
+                 lambda: f.gated_backward(x, x, x), lambda: f.grouped_gated_dgrad(x, w, ends, x, x),
+                 lambda: f.grouped_block_gemm(q, s, w, s, ends, x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    from optimizer_step_weight_amd import ffn
+    with pytest.raises(ValueError, match="silu"):
+        ffn._act("swish")
+    with pytest.raises(ValueError, match="scales"):
+        ffn._codes(q, "q", -1, None)
+    with pytest.raises(TypeError):
+        ffn._codes(x, "q", -1, s)
+    with pytest.raises(ValueError, match="4 elements"):
+        ffn._codes(q, "q", -1, torch.zeros(5))
+    with pytest.raises(ValueError, match="contiguous"):
+        ffn._codes(q[:, ::2], "q", -1, s)
+
+
+@pytest.mark.parametrize("act", R.ACTS)
+def test_gated_formula_against_differences(act):
+    g = torch.linspace(-6, 6, 401, dtype=R.F64) + 1e-3
+    u, dh, h = torch.full_like(g, 0.7), torch.full_like(g, -1.3), 1e-6
+    (dg, du, H), _ = R.gated_grads(act, dh, g, u)
+    num = dh * u * (R.act(act, g + h)[0] - R.act(act, g - h)[0]) / (2 * h)
+    assert float((dg - num).abs().max()) < 1e-8
+    assert torch.equal(du, dh * R.act(act, g)[0]) and torch.equal(H, R.act(act, g)[0] * u)
+
+
+def test_codes_are_within_half_a_step():
+    """The rule that the GPU tests take as the reference: values come back within half a step."""
+    x = torch.randn(20, 300, generator=torch.Generator().manual_seed(1)) * torch.logspace(-30, 30, 20)[:, None]
+    for kind in (R.FP8, R.I8):
+        q, s = R.quantize(x, kind)
+        top = s.to(R.F64).repeat_interleave(128, 1)[:, :300]
+        step = 2.0 ** -4 * x.to(R.F64).abs() + 2.0 ** -10 * top if kind is R.FP8 else 0.5 * top
+        assert bool(((R.value(q, s) - x.to(R.F64)).abs() <= step * (1 + 1e-4)).all())

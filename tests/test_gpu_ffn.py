@@ -1,0 +1,448 @@
+"""The operators of include/forge_ffn.h on the GPU against their definitions, at the sizes and values where
+they can go wrong.  Tolerances count roundings: u = 2^-24 for one fp32 operation, half a step of the
+stored type for the last one, and a sum of n terms is off by at most n u times the sum of magnitudes."""
+import pytest
+import torch
+
+from tests import ffn_ref as R
+
+pytestmark = pytest.mark.gpu
+BF, F32, FP8, I8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int8
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24, FP8: 2.0 ** -4}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import optimizer_step_weight_amd as forge
+    forge.device_check(0)
+    return forge
+
+
+@pytest.fixture(autouse=True)
+def _name(request):
+    print("[case]", request.node.name, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def near(got, want, tol):
+    """|got - want| <= tol element by element (64-bit CPU tensors)."""
+    off = (got.cpu().to(R.F64) - want).abs() - tol
+    over = float(off.nan_to_num(float("inf"), float("inf")).max())
+    assert over <= 0, f"over by {over}"
+
+
+def same(a, b):
+    """The same bits."""
+    return torch.equal(a.cpu().contiguous().view(torch.uint8), b.cpu().contiguous().view(torch.uint8))
+
+
+def normal(shape, seed, std=1.0, dtype=BF):
+    return (std * torch.randn(shape, generator=gen(seed))).to(dtype)
+
+
+def kept(T, N, kind, seed, std=2.0, dtype=BF):
+    """Gate and up [T, 2 N] as `kind` (None: whole), their scales, and their values in 64 bits."""
+    gu = normal((T, 2 * N), seed, std, dtype)
+    if kind is None:
+        return gu, None, gu.to(R.F64)
+    q, s = R.quantize(gu.view(2 * T, N), kind)
+    return q.view(T, 2 * N), s.view(T, -1), R.value(q, s).view(T, 2 * N)
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+# ------------------------------------------------------------------ codes of rows
+@pytest.mark.parametrize("D", [1, 7, 8, 120, 127, 128, 129, 136, 1000, 1408, 5120])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("kind", [FP8, I8])
+def test_quantize_and_back(lib, D, dt, kind):
+    """Bitwise the header's rule, with rows of zeros, of tiny and of huge values."""
+    for T in (1, 3, 70):
+        x = normal((T, D), D + T, 1.0, F32)
+        x[:, ::17] *= 30.0
+        if T > 5:
+            x[1], x[2] = 0.0, x[2] * 1e-39
+            x[3], x[4] = x[3] * 1e36, x[4] * 1e-36
+        x = x.to(dt)
+        want, scale = R.quantize(x, kind)
+        q = torch.full((T, D), 77 if kind is I8 else 7.0).to(kind).cuda()
+        s = torch.full((T, -(-D // 128)), float("nan"), device="cuda")
+        lib.block_quantize(x.cuda(), q, s)
+        assert same(s, scale) and same(q, want)
+        for out in (F32, BF):
+            y = torch.full((T, D), float("nan"), dtype=out, device="cuda")
+            lib.block_dequantize(q, s, y)
+            assert same(y, R.value(want, scale, F32).to(out))
+
+
+@pytest.mark.parametrize("kind", [FP8, I8])
+@pytest.mark.parametrize("D", [256, 300])
+def test_quantize_bad_values_spoil_their_block(lib, kind, D):
+    x = normal((6, D), 1, 1.0, F32)
+    x[1, 5], x[2, 130], x[3, D - 1], x[4, 0] = float("nan"), float("inf"), float("-inf"), -float("nan")
+    want, scale = R.quantize(x, kind)
+    q, s, y = torch.empty(6, D, dtype=kind, device="cuda"), torch.empty(6, -(-D // 128), device="cuda"), torch.empty(6, D, device="cuda")
+    lib.block_quantize(x.cuda(), q, s)
+    lib.block_dequantize(q, s, y)
+    assert same(q, want) and torch.equal(torch.isnan(s).cpu(), torch.isnan(scale))
+    bad = R.blocks(~torch.isfinite(x)).any(-1).repeat_interleave(128, 1)[:, :D]
+    assert torch.equal(torch.isnan(y).cpu(), bad)
+    assert torch.equal(y.cpu()[~bad], R.value(want, scale, F32)[~bad])
+
+
+def test_quantize_neighbouring_rows_stay(lib):
+    """Nothing past the tensor is written (views into larger buffers)."""
+    T, D = 5, 200
+    buf = torch.full((T * D + 64,), 5, dtype=I8, device="cuda")
+    sb = torch.full((T * 2 + 8,), 3.0, device="cuda")
+    x = normal((T, D), 3).cuda()
+    lib.block_quantize(x, buf[:T * D].view(T, D), sb[:T * 2].view(T, 2))
+    assert bool((buf[T * D:] == 5).all()) and bool((sb[T * 2:] == 3.0).all())
+    yb = torch.full((T * D + 64,), 9.0, dtype=BF, device="cuda")
+    lib.block_dequantize(buf[:T * D].view(T, D), sb[:T * 2].view(T, 2), yb[:T * D].view(T, D))
+    assert bool((yb[T * D:] == 9.0).all())
+
+
+def test_quantize_past_32_bits(lib):
+    """More than 2^32 codes; rows at both ends and in the middle."""
+    T, D = 300_001, 16384
+    x = torch.zeros(T, D, dtype=BF, device="cuda")
+    rows = [0, 1, 131_071, 131_072, 262_143, 262_144, T - 1]
+    vals = normal((len(rows), D), 9)
+    x[rows] = vals.cuda()
+    q, s = torch.empty(T, D, dtype=I8, device="cuda"), torch.empty(T, D // 128, device="cuda")
+    lib.block_quantize(x, q, s)
+    want, scale = R.quantize(vals, I8)
+    assert same(q[rows], want) and same(s[rows], scale)
+    lib.block_dequantize(q, s, x)
+    assert same(x[rows], R.value(want, scale, F32).to(BF))
+    assert not bool(x[2:1000].any())
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 128, 128), (3, 256, 384), (2, 1408, 640)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_quantize_weight(lib, E, N, K, dt):
+    W = normal((E, N, K), N, 0.05, F32)
+    W[0, :128, :128] = 0.0
+    W[-1, N - 1, K - 1] = 1e30
+    W = W.to(dt)
+    want, scale = R.quantize_weight(W)
+    q, qt = torch.empty(E, N, K, dtype=FP8, device="cuda"), torch.empty(E, K, N, dtype=FP8, device="cuda")
+    s, st = torch.empty(E, N // 128, K // 128, device="cuda"), torch.empty(E, K // 128, N // 128, device="cuda")
+    lib.block_quantize_weight(W.cuda(), q, s, qt=qt, scale_t=st)
+    assert same(q, want) and same(s, scale)
+    assert same(qt, want.view(torch.uint8).transpose(1, 2)) and same(st, scale.transpose(1, 2))
+    q2, s2 = torch.empty_like(q), torch.empty_like(s)
+    lib.block_quantize_weight(W.cuda() if E > 1 else W[0].cuda(), q2 if E > 1 else q2[0], s2)
+    assert same(q2, q) and same(s2, s)
+    W[0, 5, 5] = float("nan")
+    lib.block_quantize_weight(W.cuda(), q, s)
+    assert bool(torch.isnan(s[0, 0, 0])) and int(torch.isnan(s).sum()) == 1
+    assert not bool(q[0, :128, :128].view(torch.uint8).any())
+
+
+# ------------------------------------------------------------------ the activation's backward pass
+@pytest.mark.parametrize("act", R.ACTS)
+@pytest.mark.parametrize("N", [1, 9, 128, 200, 1408])
+def test_gated_backward(lib, act, N):
+    for T in (1, 37):
+        for dt, kind in ((BF, None), (BF, FP8), (BF, I8), (F32, None), (F32, FP8), (F32, I8)):
+            gu, s, v = kept(T, N, kind, N + T, 3.0, dt)
+            dh = normal((T, N), 5, 1.0, dt)
+            want, off = R.gated_grads(act, dh.to(R.F64), v[:, :N], v[:, N:])
+            # the values that codes stand for are rounded to fp32 themselves
+            extra = 0.0 if kind is None else 4 * R.U
+            d, H = torch.full((T, 2 * N), float("nan"), dtype=dt, device="cuda"), torch.full((T, N), float("nan"), dtype=dt, device="cuda")
+            lib.gated_backward(dh.cuda(), gu.cuda(), d, H=H, gate_up_scale=dev(s), act=act)
+            for got, w, o in zip((d[:, :N], d[:, N:], H), want, off):
+                o = o + extra * (1 + v[:, :N].abs()) * ((dh.to(R.F64).abs() + v[:, N:].abs()) * (1 + v.abs().amax()))
+                near(got, w, o + HALF[dt] * (w.abs() + o) + 2.0 ** -133)
+            d2 = torch.empty_like(d)
+            lib.gated_backward(dh.cuda(), gu.cuda(), d2, gate_up_scale=dev(s), act=act)
+            assert torch.equal(d, d2)
+            if kind is None:    # in place
+                gud, dhd = gu.cuda(), dh.cuda()
+                lib.gated_backward(dhd, gud, gud, H=dhd, act=act)
+                assert torch.equal(gud, d) and torch.equal(dhd, H)
+
+
+@pytest.mark.parametrize("act", R.ACTS)
+def test_gated_backward_far_gates(lib, act):
+    """Gates where the activation saturates: finite, and right to their own size."""
+    g = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 12.0, -12.0, 40.0, -40.0, 90.0, -90.0, 300.0, -300.0, 1e10, -1e10,
+                      1e18, -1e18, 3e38, -3e38])
+    N = g.numel()
+    u, dh = torch.full((1, N), 0.5), torch.full((1, N), 0.25)
+    d, H = torch.empty(1, 2 * N, device="cuda"), torch.empty(1, N, device="cuda")
+    lib.gated_backward(dh.cuda(), torch.cat([g[None], u], 1).cuda(), d, H=H, act=act)
+    if act == "gelu_tanh":     # the definition's g^3 leaves 64 bits; past 64 it is at its limit
+        v = g.to(R.F64)[None].clamp(-64, 64)
+        a, s = R.act(act, v)
+        a = torch.where(g[None].abs() > 64, g.to(R.F64)[None].clamp(min=0), a)
+    else:
+        v = g.to(R.F64)[None]
+        a, s = R.act(act, v)
+        s = torch.where(torch.isnan(s), (v > 0).to(R.F64), s)
+    ea, es = R.act_error(act, v)
+    es = torch.where(v.abs() > 90, 2.0 ** -22, es.nan_to_num(0, 0))
+    ea = torch.where(v.abs() > 60, a.abs() * 2.0 ** -18, ea) + 2.0 ** -126 * g.abs().to(R.F64)
+    near(H, a / 2, ea + 4 * R.U * a.abs())
+    near(d[:, N:], a / 4, ea + 4 * R.U * a.abs())
+    near(d[:, :N], s / 8, es + 2.0 ** -100)
+
+
+# ------------------------------------------------------------------ the products
+def ends_of(T, E, seed):
+    e = torch.randint(0, T + 1, (E,), generator=gen(seed)).sort().values.to(torch.int32)
+    return e
+
+
+SHAPES = [(1, 1, 128, 128), (1, 1, 256, 256), (5, 3, 384, 128), (33, 2, 128, 640), (100, 1, 1408, 256), (200, 64, 256, 384), (300, 4, 512, 512),
+          (515, 2, 640, 320 + 64), (1030, 1, 2048 + 128, 128)]
+
+
+@pytest.mark.parametrize("T,E,N,K", SHAPES)
+@pytest.mark.parametrize("kind", ["none", BF, FP8, I8])
+def test_grouped_gated(lib, T, E, N, K, kind):
+    """Every height of tile, narrow and wide ones, empty groups and rows of no group."""
+    act = R.ACTS[(T + E) % 4]
+    X, W = normal((T, K), T), normal((E, 2 * N, K), N, K ** -0.5)
+    ends = ends_of(T, E, T)
+    if T % 2:
+        ends[-1] = T
+    gu, mag = R.grouped(X, W, ends, True)
+    g, u, off = gu[:, :N], gu[:, N:], K * R.U * mag
+    a, _ = R.act(act, g)
+    ea, _ = R.act_error(act, g)
+    H = torch.full((T, N), float("nan"), dtype=BF, device="cuda")
+    out = s = None
+    if kind != "none":
+        out = torch.full((T, 2 * N), 1.0).to(kind).cuda()
+        s = None if kind is BF else torch.full((T, 2, N // 128), float("nan"), device="cuda")
+    lib.grouped_gated(X.cuda(), W.cuda(), ends.cuda(), H, gate_up=out, gate_up_scale=s, act=act)
+    # no slope of the activations exceeds 1.2
+    oh = u.abs() * (1.2 * off[:, :N] + ea) + (a.abs() + 1.2 * off[:, :N]) * off[:, N:] + 2 * R.U * (a * u).abs()
+    near(H, a * u, oh + HALF[BF] * ((a * u).abs() + oh) + 2.0 ** -133)
+    rest = R.spans(ends, T)[1]
+    assert not bool(H[rest[0]:].any())
+    if kind is BF:
+        near(out, gu, off + HALF[BF] * (gu.abs() + off) + 2.0 ** -133)
+    elif kind in (FP8, I8):
+        got = R.value(out.cpu(), s.cpu().view(T, -1))
+        top = s.cpu().to(R.F64).view(T, -1).repeat_interleave(128, 1)
+        near(s.view(T, -1), R.blocks(gu).abs().amax(-1).div(R.MOST[kind]).clamp(min=2.0 ** -126),
+             R.blocks(off).amax(-1) / R.MOST[kind] + 2 * R.U * s.cpu().to(R.F64).view(T, -1))
+        # half a step of the code (its quotient rounded twice) and the sum's own error
+        step = HALF[FP8] * gu.abs() + 2.0 ** -10 * top if kind is FP8 else 0.5 * top
+        near(got, gu, (1 + 8 * R.U * R.MOST[kind]) * step + 1.1 * off)
+        h2 = torch.empty_like(H)
+        lib.grouped_gated(X.cuda(), W.cuda(), ends.cuda(), h2, act=act)
+        near(h2, H.cpu().to(R.F64), 2 * HALF[BF] * H.cpu().to(R.F64).abs() + 2 * oh)
+
+
+@pytest.mark.parametrize("T,E,N,K", SHAPES)
+@pytest.mark.parametrize("kind", [None, FP8, I8])
+def test_grouped_gated_dgrad(lib, T, E, N, K, kind):
+    act = R.ACTS[(T + E + 1) % 4]
+    dY, W = normal((T, K), T + 1), normal((E, K, N), N + 1, K ** -0.5)
+    ends = ends_of(T, E, T + 1)
+    if T % 2:
+        ends[-1] = T
+    gu, s, v = kept(T, N, kind, T + 2)
+    last = R.spans(ends, T)[1][0]
+    if last < T and kind is None:
+        gu[last:] = float("nan")       # of no group
+    dh, mag = R.grouped(dY, W, ends, False)
+    v[last:] = 0
+    want, off = R.gated_grads(act, dh, v[:, :N], v[:, N:])
+    a, slope = R.act(act, v[:, :N])
+    oh = K * R.U * mag
+    off = (off[0] + oh * (v[:, N:] * slope).abs(), off[1] + oh * a.abs(), off[2])
+    off = tuple(o + (0.0 if kind is None else 16 * R.U) * ((1 + v[:, :N].abs()) * (1 + v[:, N:].abs()) * (1 + dh.abs())) for o in off)
+    d, H = torch.full((T, 2 * N), float("nan"), dtype=BF, device="cuda"), torch.full((T, N), float("nan"), dtype=BF, device="cuda")
+    lib.grouped_gated_dgrad(dY.cuda(), W.cuda(), ends.cuda(), gu.cuda(), d, H=H, gate_up_scale=dev(s), act=act)
+    for got, w, o in zip((d[:, :N], d[:, N:], H), want, off):
+        near(got, w, o + HALF[BF] * (w.abs() + o) + 2.0 ** -133)
+    d2 = torch.empty_like(d)
+    lib.grouped_gated_dgrad(dY.cuda(), W.cuda(), ends.cuda(), gu.cuda(), d2, gate_up_scale=dev(s), act=act)
+    assert torch.equal(d, d2)
+    if kind is None:
+        gud = gu.cuda()
+        lib.grouped_gated_dgrad(dY.cuda(), W.cuda(), ends.cuda(), gud, gud, act=act)
+        assert torch.equal(gud, d)
+
+
+def test_gated_bad_rows_stay_apart(lib):
+    """NaN and infinities of one group, or of rows of no group, reach no other row."""
+    T, N, K, ends = 250, 256, 256, torch.tensor([70, 140, 210], dtype=torch.int32)
+    X, W = normal((T, K), 1), normal((3, 2 * N, K), 2, K ** -0.5)
+    dY, Wd = normal((T, K), 3), normal((3, K, N), 4, K ** -0.5)
+    gu, _, _ = kept(T, N, None, 5)
+    H, H1 = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, N, dtype=BF, device="cuda")
+    d, d1 = torch.empty(T, 2 * N, dtype=BF, device="cuda"), torch.empty(T, 2 * N, dtype=BF, device="cuda")
+    lib.grouped_gated(X.cuda(), W.cuda(), ends.cuda(), H)
+    lib.grouped_gated_dgrad(dY.cuda(), Wd.cuda(), ends.cuda(), gu.cuda(), d)
+    X[70:140], dY[70:140], X[210:], dY[210:], gu[210:] = float("nan"), float("nan"), float("nan"), float("inf"), float("nan")
+    lib.grouped_gated(X.cuda(), W.cuda(), ends.cuda(), H1)
+    lib.grouped_gated_dgrad(dY.cuda(), Wd.cuda(), ends.cuda(), gu.cuda(), d1)
+    ok = torch.cat([torch.arange(70), torch.arange(140, 250)])
+    assert torch.equal(H.cpu()[ok], H1.cpu()[ok]) and torch.equal(d.cpu()[ok], d1.cpu()[ok])
+    assert torch.isnan(H1[70:140]).all() and not bool(H1[210:].any()) and not bool(d1[210:].any())
+
+
+def codes(shape, seed):
+    """Every finite code of e4m3 alike."""
+    u = torch.randint(0, 256, shape, generator=gen(seed), dtype=torch.int16)
+    return torch.where((u & 127) == 127, u - 1, u).to(torch.uint8).view(FP8)
+
+
+def block_reference(X, xs, W, ws, ends):
+    """Y and how far it may be off: in each block the matrix unit cuts the products of eight consecutive
+    elements at 2^-13 of the largest one's power of two and adds with at most a step of fp32 a term;
+    then come the scales' product, its product with the sum, and the sum over blocks."""
+    T, K = X.shape
+    N, KB = W.shape[1], K // 128
+    Y, off = torch.zeros(T, N, dtype=R.F64), torch.zeros(T, N, dtype=R.F64)
+    for e, (a, b) in enumerate(R.spans(ends, T)[0]):
+        if a == b:
+            continue
+        mag = torch.zeros(b - a, N, dtype=R.F64)
+        for k in range(KB):
+            x, w = X[a:b, 128 * k:128 * k + 128].to(R.F64), W[e, :, 128 * k:128 * k + 128].to(R.F64)
+            s = xs[a:b, k].to(R.F64)[:, None] * ws[e, :, k].to(R.F64).repeat_interleave(128)[None]
+            eights = lambda z: z.abs().unflatten(-1, (-1, 8)).amax(-1)  # noqa: E731
+            Y[a:b] += (x @ w.t()) * s
+            m = (x.abs() @ w.abs().t()) * s
+            off[a:b] += 7 * 2.0 ** -13 * (eights(x) @ eights(w).t()) * s + (256 + 3) * R.U * m
+            mag += m
+        off[a:b] += KB * R.U * mag
+    return Y, off
+
+
+@pytest.mark.parametrize("T,E,N,K", [s if s[3] % 128 == 0 else (s[0], s[1], s[2], 384) for s in SHAPES] + [(70, 2, 128, 2176), (8, 1, 512, 4096)])
+def test_block_product(lib, T, E, N, K):
+    X, W = codes((T, K), T), codes((E, N, K), N)
+    g = gen(3)
+    xs, ws = 0.1 + torch.rand(T, K // 128, generator=g), 0.003 * (0.1 + torch.rand(E, N // 128, K // 128, generator=g))
+    ends = ends_of(T, E, T)
+    if T % 2 == 0:
+        ends[-1] = T
+    Y = torch.full((T, N), float("nan"), dtype=BF, device="cuda")
+    lib.grouped_block_gemm(X.cuda(), xs.cuda(), W.cuda(), ws.cuda(), ends.cuda(), Y)
+    want, off = block_reference(X, xs, W, ws, ends)
+    near(Y, want, off + HALF[BF] * (want.abs() + off) + 2.0 ** -133)
+    again = torch.zeros_like(Y)
+    lib.grouped_block_gemm(X.cuda(), xs.cuda(), W.cuda(), ws.cuda(), ends.cuda(), again)
+    assert torch.equal(Y, again)
+
+
+def test_block_product_exact_and_bad_blocks(lib):
+    """Small whole numbers and scales that are powers of two: exact.  A NaN scale or code spoils its row, or its
+    columns of its group, alone."""
+    T, E, N, K, ends = 300, 2, 384, 512, [130, 280]
+    X = torch.randint(-3, 4, (T, K), generator=gen(1)).float().to(FP8)
+    W = torch.randint(-3, 4, (E, N, K), generator=gen(2)).float().to(FP8)
+    xs = 2.0 ** torch.randint(-3, 4, (T, K // 128), generator=gen(3)).float()
+    ws = 2.0 ** torch.randint(-3, 4, (E, N // 128, K // 128), generator=gen(4)).float()
+    ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    Y = torch.empty(T, N, dtype=BF, device="cuda")
+    lib.grouped_block_gemm(X.cuda(), xs.cuda(), W.cuda(), ws.cuda(), ed, Y)
+    want = block_reference(X, xs, W, ws, ends)[0]
+    assert torch.equal(Y.cpu(), want.to(BF))
+    xs[7, 2], ws[1, 2, 3] = float("nan"), float("nan")
+    X.view(torch.uint8)[9, 100] = 0x7F
+    X[290:], xs[295:] = float("nan"), float("nan")
+    lib.grouped_block_gemm(X.cuda(), xs.cuda(), W.cuda(), ws.cuda(), ed, Y)
+    bad = torch.zeros(T, N, dtype=torch.bool)
+    bad[7], bad[9], bad[130:280, 256:] = True, True, True
+    assert torch.isnan(Y.cpu()[bad]).all() and torch.equal(Y.cpu()[~bad], want.to(BF)[~bad])
+
+
+# ------------------------------------------------------------------ the norm's backward pass from codes
+@pytest.mark.parametrize("D", [1, 100, 130, 512, 520, 2048, 4096, 5120, 8200, 16384, 16500])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("kind", [FP8, I8])
+def test_norm_backward_of_codes(lib, D, dt, kind):
+    """As the same call on what the codes stand for, where fp32 holds it."""
+    for T in (1, 6, 67):
+        h, gain = normal((T, D), D + T, 1.0, F32), 1 + normal((D,), 1, 0.3, F32)
+        rstd = torch.rsqrt((h * h).mean(1) + 1e-6)
+        q, s = R.quantize(h, kind)
+        dy, dh = normal((T, D), 2, 1.0, dt), normal((T, D), 3, 1.0, dt)
+        qd, sd, gd, rd = q.cuda(), s.cuda(), gain.cuda(), rstd.cuda()
+        value = torch.empty(T, D, device="cuda")
+        lib.block_dequantize(qd, sd, value)
+        for res in (None, dh.cuda()):
+            dx, dg = torch.empty(T, D, dtype=dt, device="cuda"), torch.empty(D, device="cuda")
+            lib.rmsnorm_backward(dy.cuda(), qd, gd, rd, dx, dg, dh=res, h_scale=sd)
+            want, dgw = torch.empty(T, D, device="cuda"), torch.empty(D, device="cuda")
+            lib.rmsnorm_backward(dy.float().cuda(), value, gd, rd, want, dgw, dh=None if res is None else res.float())
+            assert torch.equal(dx, want.to(dt)) and torch.equal(dg, dgw)
+            dx2 = torch.empty_like(dx)
+            lib.rmsnorm_backward(dy.cuda(), qd, gd, rd, dx2, dh=res, h_scale=sd)
+            assert torch.equal(dx, dx2)
+
+
+# ------------------------------------------------------------------ together
+def test_block_of_a_layer(lib):
+    """Forward with codes kept, backward from them, the input gradient and the weights' step, as one training step of
+    a gated block calls them; every stage against the definition of what it was given."""
+    T, E, N, K, act = 333, 3, 384, 256, "silu"
+    ends = torch.tensor([100, 100, 320], dtype=torch.int32)
+    X, W, Wd = normal((T, K), 1), normal((E, 2 * N, K), 2, K ** -0.5), normal((E, K, N), 3, N ** -0.5)
+    dY = normal((T, K), 4)
+    Xd, Wc, Wdc, ed, dYc = X.cuda(), W.cuda(), Wd.cuda(), ends.cuda(), dY.cuda()
+    H, gu = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, 2 * N, dtype=I8, device="cuda")
+    s, Y = torch.empty(T, 2, N // 128, device="cuda"), torch.empty(T, K, dtype=BF, device="cuda")
+    lib.grouped_gated(Xd, Wc, ed, H, gate_up=gu, gate_up_scale=s, act=act)
+    lib.grouped_gemm(H, Wdc, ed, Y)
+    d, H2, dX = torch.empty(T, 2 * N, dtype=BF, device="cuda"), torch.empty_like(H), torch.empty_like(Xd)
+    lib.grouped_gated_dgrad(dYc, Wdc, ed, gu, d, H=H2, gate_up_scale=s, act=act)
+    lib.grouped_dgrad(d, Wc, ed, dX)
+    dW, dWd = torch.empty(E, 2 * N, K, device="cuda"), torch.empty(E, K, N, device="cuda")
+    lib.grouped_wgrad(Xd, d, ed, dW)
+    lib.grouped_wgrad(H2, dYc, ed, dWd)
+    # autograd in 64 bits of the whole block at the values kept: relative to the largest, as 8-bit codes (1 / 254 of a
+    # block's largest) and bf16 leave it
+    v = R.value(gu.cpu(), s.cpu().view(T, -1))
+    (dg, du, h), _ = R.gated_grads(act, R.grouped(dY, Wd, ends, False)[0], v[:, :N], v[:, N:])
+    want = R.grouped(torch.cat([dg, du], 1), W, ends, False)[0]
+    mag = R.grouped(torch.cat([dg, du], 1).abs(), W.abs(), ends, False)[1]
+    near(dX, want, HALF[BF] * (want.abs() + 2 * mag))
+    for got, a, b in ((dW, X, torch.cat([dg, du], 1)), (dWd, h, dY)):
+        from tests.layer_ref import grouped_wgrad
+        near(got, grouped_wgrad(a, b, ends), 2 * HALF[BF] * grouped_wgrad(a.abs(), b.abs(), ends) + 1e-30)
+
+
+def test_block_gradients_against_differences(lib):
+    """The gradient of sum(c * Y) by the backward pass against central differences of the forward formula in 64 bits."""
+    T, N, K, act = 4, 128, 128, "gelu_tanh"
+    X, W, Wd = normal((T, K), 1), normal((1, 2 * N, K), 2, K ** -0.5), normal((1, K, N), 3, N ** -0.5)
+    c = normal((T, K), 4)
+    ends = torch.tensor([T], dtype=torch.int32)
+
+    def loss(x):
+        gu = x @ W[0].to(R.F64).t()
+        h = R.act(act, gu[:, :N])[0] * gu[:, N:]
+        return float((h @ Wd[0].to(R.F64).t() * c.to(R.F64)).sum())
+    gu, H = torch.empty(T, 2 * N, dtype=BF, device="cuda"), torch.empty(T, N, dtype=BF, device="cuda")
+    d, dX = torch.empty(T, 2 * N, dtype=BF, device="cuda"), torch.empty(T, K, dtype=BF, device="cuda")
+    lib.grouped_gated(X.cuda(), W.cuda(), ends.cuda(), H, gate_up=gu, act=act)
+    lib.grouped_gated_dgrad(c.cuda(), Wd.cuda(), ends.cuda(), gu, d, act=act)
+    lib.grouped_dgrad(d, W.cuda(), ends.cuda(), dX)
+    for seed in range(3):
+        v = normal((T, K), 10 + seed).to(R.F64)
+        x, h = X.to(R.F64), 1e-4
+        slope = (loss(x + h * v) - loss(x - h * v)) / (2 * h)
+        got = float((dX.cpu().to(R.F64) * v).sum())
+        # gate, up, d(gate, up) and dX are each rounded to bf16: half a step of the sums of magnitudes, roughly in quadrature
+        # over N K T terms; the bound is the plain sum of magnitudes
+        size = float((dX.cpu().to(R.F64).abs() * v.abs()).sum())
+        assert abs(got - slope) <= 4 * HALF[BF] * size
