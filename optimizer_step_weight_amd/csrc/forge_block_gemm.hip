@@ -2,13 +2,16 @@
 // 128 x 128 of W:  Y[t, n] = sum over b of sx[t, b] sw[n / 128, b] sum over k in block b of X[t, k] W[n, k].
 //
 // A block's sum is multiplied by its scales before the next is added, so the matrix cores cannot keep the
-// whole contraction in their accumulators: each 32 x 32 block of the output takes two 32 x 32 x 64 products
-// from zero (128 of the contraction, 128 cycles) and 16 multiply-adds on the vector unit (64 cycles), which
-// run beside the next block's products.  The vector unit cannot read the accumulation registers, so a wave
-// keeps 128 x 64 of the output in 128 vector registers, and 8 waves (two a SIMD) a tile of 256 x 256.
+// whole contraction in their accumulators: each 16 x 16 block of the output takes one 16 x 16 x 128 product
+// from zero (32 cycles) and 4 multiply-adds on the vector unit (16 cycles), which run beside the next
+// block's products.  The vector unit cannot read the accumulation registers, so a wave keeps 128 x 64 of
+// the output in 128 vector registers, and 8 waves (two a SIMD) a tile of 256 x 256.  (32 x 32 x 64 products,
+// two from zero for each block, need 32 registers instead of 16 for results that wait.)
 //
 // A slab is one block of the contraction, 128 bytes of a row, copied to LDS by DMA in whole lines; LDS holds
 // two.  The scales of 8 slabs are loaded 8 slabs ahead and pass through LDS, by slab and row.
+//
+// 16384 rows of 8 uneven experts by 14336 x 4096: 1038 us, 1.85 PFLOP/s.
 #include <hip/hip_runtime.h>
 
 #include "forge_ffn_internal.h"
@@ -26,31 +29,31 @@ constexpr int SCALES_AT = 2 * STAGE_LDS, SCALES_LDS = (CHUNK * 256 + 2 * CHUNK) 
 
 __device__ __forceinline__ int block_swz(int row) { return (row >> 1) & 7; }
 
-template <int MB, int NB>  // blocks of 32 rows and columns of a wave: a tile of 64 MB rows and 128 NB columns
+template <int HEIGHT, int WIDTH>  // of the tile, in 64s
 __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile& t, unsigned char* smem) {
+  constexpr int MB = 2 * HEIGHT, NB = WIDTH;   // blocks of 16 rows and columns of a wave (2 x 4 waves)
+  constexpr int DX = HEIGHT, DW = WIDTH;       // copies of 1 KiB of a wave a slab
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wr = wave >> 2, wc = wave & 3;
   const int64_t n0 = (int64_t)t.n * t.cols;
   const int KB = (int)(a.K / 128), slabs = t.e < a.E ? KB : 0;
   const uint32_t ld = (uint32_t)a.K;
   const u32x4 rx = make_rsrc(a.X + (int64_t)t.row0 * a.K, (uint32_t)t.rows * ld);
-  const u32x4 rw = make_rsrc(a.W + ((int64_t)t.e * a.N + n0) * a.K, (uint32_t)(128 * NB) * ld);
+  const u32x4 rw = make_rsrc(a.W + ((int64_t)t.e * a.N + n0) * a.K, (uint32_t)(64 * WIDTH) * ld);
   const uint32_t lds = lds_address(smem);
-  uint32_t ox[MB], ow[2 * NB];  // this lane's pieces of the wave's copies
+  uint32_t ox[DX], ow[DW];  // this lane's pieces of the wave's copies
+  auto piece_of = [&](int copy) {
+    const int r = 8 * copy + (lane >> 3);
+    return (uint32_t)r * ld + 16u * (uint32_t)((lane & 7) ^ block_swz(r));
+  };
 #pragma unroll
-  for (int j = 0; j < MB; ++j) {
-    const int r = 8 * (MB * wave + j) + (lane >> 3);
-    ox[j] = (uint32_t)r * ld + 16u * (uint32_t)((lane & 7) ^ block_swz(r));
-  }
+  for (int j = 0; j < DX; ++j) ox[j] = piece_of(DX * wave + j);
 #pragma unroll
-  for (int j = 0; j < 2 * NB; ++j) {
-    const int r = 8 * (2 * NB * wave + j) + (lane >> 3);
-    ow[j] = (uint32_t)r * ld + 16u * (uint32_t)((lane & 7) ^ block_swz(r));
-  }
+  for (int j = 0; j < DW; ++j) ow[j] = piece_of(DW * wave + j);
   auto copy = [&](int s) {
     const uint32_t at = lds + (uint32_t)((s & 1) * STAGE_LDS), k = (uint32_t)s * 128u;
-    static_for<MB>([&](auto j) { copy_1k<j * 1024>(rx, ox[j] + k, at + (uint32_t)(wave * MB * 1024)); });
-    static_for<2 * NB>([&](auto j) { copy_1k<PANEL_LDS + j * 1024>(rw, ow[j] + k, at + (uint32_t)(wave * 2 * NB * 1024)); });
+    static_for<DX>([&](auto j) { copy_1k<j * 1024>(rx, ox[j] + k, at + (uint32_t)(wave * DX * 1024)); });
+    static_for<DW>([&](auto j) { copy_1k<PANEL_LDS + j * 1024>(rw, ow[j] + k, at + (uint32_t)(wave * DW * 1024)); });
   };
   // Scales: two threads a row of X, four slabs each; 2 x 8 threads those of W.
   auto scales = [&](int chunk) { return reinterpret_cast<float*>(smem + SCALES_AT + (chunk & 1) * SCALES_LDS); };
@@ -63,7 +66,7 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
       const int s = s0 + sh + j;
       sx[j] = sr < t.rows && s < slabs ? a.x_scale[(int64_t)(t.row0 + sr) * KB + s] : 0.0f;
     }
-    const int s = s0 + ((int)threadIdx.x & (CHUNK - 1)), b = ((int)threadIdx.x / CHUNK) & (NB - 1);
+    const int s = s0 + ((int)threadIdx.x & (CHUNK - 1)), b = WIDTH == 4 ? ((int)threadIdx.x / CHUNK) & 1 : 0;
     sw = s < slabs ? a.w_scale[((int64_t)t.e * (a.N / 128) + n0 / 128 + b) * KB + s] : 0.0f;
   };
   auto put_scales = [&](int chunk) {
@@ -73,28 +76,24 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
     if (threadIdx.x < 2 * CHUNK) p[CHUNK * 256 + threadIdx.x] = sw;
   };
 
-  floatx16 acc[MB][NB];
+  floatx4 acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = floatx16{};
+    for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{};
   if (slabs > 0) {
     copy(0);
     fetch_scales(0);
     put_scales(0);
   }
-  // addresses of a row's pieces: the row's swizzle is the same in every block of 32
-  const int row = lane & 31, q = 2 * (lane >> 5);
-  uint32_t piece[4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x) piece[x] = (uint32_t)(row * 128 + 16 * ((4 * (x >> 1) + q + (x & 1)) ^ block_swz(row)));
+  // addresses of a lane's two pieces: the row's swizzle is the same in every block of 16
+  const int row = lane & 15, q = lane >> 4;
+  const uint32_t piece0 = (uint32_t)(row * 128 + 16 * ((2 * q) ^ block_swz(row)));
+  const uint32_t piece1 = (uint32_t)(row * 128 + 16 * ((2 * q + 1) ^ block_swz(row)));
   using P4 = __attribute__((address_space(3))) const u32x4*;
-  auto frag = [&](uint32_t panel, int half) {
-    const u32x4 lo = *(P4)(panel + piece[2 * half]), hi = *(P4)(panel + piece[2 * half + 1]);
+  auto frag = [&](uint32_t p0, uint32_t p1, int block) {
+    const u32x4 lo = *(P4)(p0 + block * 2048), hi = *(P4)(p1 + block * 2048);
     return __builtin_bit_cast(intx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
-  auto product = [&](const intx8& w, const intx8& x, const floatx16& c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 0, 0, 0, 0);
   };
   for (int s = 0; s < slabs; ++s) {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -102,51 +101,52 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
     const int c = s & (CHUNK - 1);
     if (c == 0) fetch_scales(s / CHUNK + 1);
     const float* sc = scales(s / CHUNK);
-    const float w_scale = sc[CHUNK * 256 + (NB == 2 ? (wc >> 1) * CHUNK : 0) + c];
-    const uint32_t px = lds + (uint32_t)((s & 1) * STAGE_LDS + wr * MB * 4096);
-    const uint32_t pw = lds + (uint32_t)((s & 1) * STAGE_LDS + PANEL_LDS + wc * NB * 4096);
-    intx8 w[NB][2];
+    const uint32_t px = lds + (uint32_t)((s & 1) * STAGE_LDS + wr * MB * 2048);
+    const uint32_t pw = lds + (uint32_t)((s & 1) * STAGE_LDS + PANEL_LDS + wc * NB * 2048);
+    const uint32_t x0 = px + piece0, x1 = px + piece1, w0 = pw + piece0, w1 = pw + piece1;
+    intx8 w[NB], x[2];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      w[j][0] = frag(pw + j * 4096, 0);
-      w[j][1] = frag(pw + j * 4096, 1);
-    }
-    floatx16 part[2];
+    for (int j = 0; j < NB; ++j) w[j] = frag(w0, w1, j);
+    x[0] = frag(x0, x1, 0);
+    const float w_scale = sc[CHUNK * 256 + (WIDTH == 4 ? (wc >> 1) * CHUNK : 0) + c];
     float scale[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i) scale[i] = sc[c * 256 + wr * 32 * MB + 32 * i + row] * w_scale;
-    auto add = [&](auto bc) {
-      constexpr int b = decltype(bc)::value, i = b / NB, j = b % NB;
+    for (int i = 0; i < MB; ++i) scale[i] = sc[c * 256 + wr * 16 * MB + 16 * i + row];
+    __builtin_amdgcn_sched_barrier(0);
+    floatx4 part[2][NB];
+    auto add = [&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      const float f = scale[i] * w_scale;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[b & 1][r], scale[i], acc[i][j][r]);
+      for (int j = 0; j < NB; ++j) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[i & 1][j][r], f, acc[i][j][r]);
+        asm volatile("" : "+v"(acc[i][j]));  // here, not after all the products: their results would not fit
+      }
     };
     static_for<MB>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      const intx8 x0 = frag(px + i * 4096, 0), x1 = frag(px + i * 4096, 1);
-      static_for<NB>([&](auto jc) {
-        constexpr int j = decltype(jc)::value, b = i * NB + j;
-        part[b & 1] = product(w[j][0], x0, floatx16{});
-        part[b & 1] = product(w[j][1], x1, part[b & 1]);
-        if constexpr (b > 0) add(std::integral_constant<int, b - 1>{});
-        __builtin_amdgcn_sched_barrier(0);
-      });
+      if constexpr (i + 1 < MB) x[(i + 1) & 1] = frag(x0, x1, i + 1);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        part[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x[i & 1], floatx4{}, 0, 0, 0, 0, 0, 0);
+      if constexpr (i > 0) add(std::integral_constant<int, i - 1>{});
+      __builtin_amdgcn_sched_barrier(0);
     });
-    add(std::integral_constant<int, MB * NB - 1>{});
+    add(std::integral_constant<int, MB - 1>{});
     if (c == CHUNK - 1) put_scales(s / CHUNK + 1);
   }
   __syncthreads();
   // out by rows through LDS in bf16: 16-byte chunks are XOR-swizzled with the row
-  constexpr int ROW = 256 * NB, CH = ROW / 16;
+  constexpr int ROW = 128 * WIDTH, CH = ROW / 16;
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int r = wr * 32 * MB + 32 * i + row, c4 = wc * 8 * NB + 8 * j + 2 * g + (lane >> 5);  // column / 4
-        *reinterpret_cast<u32x2*>(smem + r * ROW + 16 * ((c4 >> 1) ^ (r & 15)) + 8 * (c4 & 1)) =
-            u32x2{pack_bf16(acc[i][j][4 * g], acc[i][j][4 * g + 1]), pack_bf16(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3])};
-      }
+    for (int j = 0; j < NB; ++j) {
+      const int r = wr * 16 * MB + 16 * i + row, c4 = wc * 4 * NB + 4 * j + q;  // column / 4
+      *reinterpret_cast<u32x2*>(smem + r * ROW + 16 * ((c4 >> 1) ^ (r & 15)) + 8 * (c4 & 1)) =
+          u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+    }
   __syncthreads();
   for (int p = (int)threadIdx.x; p < t.rows * CH; p += BLOCK_THREADS) {
     const int r = p / CH, c = p % CH;
@@ -160,14 +160,14 @@ __global__ __launch_bounds__(BLOCK_THREADS, 2) void block_gemm_kernel(BlockGemmA
   if (!find_tile<256>(a.ends, a.E, a.T, a.N, a.cols, (int)blockIdx.x, t)) return;
   const bool narrow = t.cols < 256 || a.N - (int64_t)t.n * 256 < 256;
   switch ((t.rows + 63) / 64 + (narrow ? 4 : 0)) {
-    case 1: block_tile<1, 2>(a, t, smem); break;
-    case 2: block_tile<2, 2>(a, t, smem); break;
-    case 3: block_tile<3, 2>(a, t, smem); break;
-    case 4: block_tile<4, 2>(a, t, smem); break;
-    case 5: block_tile<1, 1>(a, t, smem); break;
-    case 6: block_tile<2, 1>(a, t, smem); break;
-    case 7: block_tile<3, 1>(a, t, smem); break;
-    case 8: block_tile<4, 1>(a, t, smem); break;
+    case 1: block_tile<1, 4>(a, t, smem); break;
+    case 2: block_tile<2, 4>(a, t, smem); break;
+    case 3: block_tile<3, 4>(a, t, smem); break;
+    case 4: block_tile<4, 4>(a, t, smem); break;
+    case 5: block_tile<1, 2>(a, t, smem); break;
+    case 6: block_tile<2, 2>(a, t, smem); break;
+    case 7: block_tile<3, 2>(a, t, smem); break;
+    case 8: block_tile<4, 2>(a, t, smem); break;
   }
 }
 
