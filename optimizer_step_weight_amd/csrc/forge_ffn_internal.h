@@ -30,6 +30,7 @@ struct GatedArgs {
   int64_t T, N, K;
 };
 int launch_grouped_gated(const GatedArgs& a, void* stream);
+int launch_gated_few(const GatedArgs& a, void* stream);  // 8-bit gate and up: not there
 
 // dH = dY W, W [E, K, N]; from it and the kept gate and up d(gate, up) and H.
 struct GatedDgradArgs {
@@ -92,5 +93,17 @@ struct BlockGemmArgs {
   int64_t T, N, K;
 };
 int launch_grouped_block_gemm(const BlockGemmArgs& a, void* stream);
+int launch_block_few(const BlockGemmArgs& a, void* stream);
+// Whether the kernels of few rows (forge_few.hip) take a call, by the least tiles of the other kernels that its rows
+// and columns make: these are slow where they leave CUs without any, those read X again for each 16 columns.
+// In us, few rows against tiles, one weight: gated product of 4096 x 4096 (64 tiles) 17 against 43 at 16 rows, 29
+// against 42 at 64, 54 against 44 at 128; of 8192 x 2048 (128 tiles) 21 against 26 at 32 rows, 32 against 26 at 64; of
+// 14336 x 4096 (224 tiles) 49 against 46 at 1.  Block product of 4096 x 14336 (32 tiles) 22 against 97 at 16 rows, 95
+// against 142 at 128; of 14336 x 4096 (112 tiles) 35 against 42 at 32 rows, 61 against 44 at 64; of 2048 x 4096 (16 tiles)
+// 32 against 41 at 256.
+inline bool few_rows_call(int64_t T, int32_t E, int64_t N, int64_t cols) {
+  const int64_t tiles = (E < T ? E : T) * (N / cols);
+  return T <= 256 && tiles <= 128 && T * tiles <= 4096;
+}
 
 }  // namespace forge

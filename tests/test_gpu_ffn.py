@@ -297,6 +297,17 @@ def test_gated_bad_rows_stay_apart(lib):
     assert torch.isnan(H1[70:140]).all() and not bool(H1[210:].any()) and not bool(d1[210:].any())
 
 
+FEW = [(3, 1, 128, 192), (16, 2, 256, 1088), (17, 1, 384, 320), (31, 5, 128, 64 * 17), (64, 1, 512, 576), (100, 2, 128, 256), (256, 1, 128, 384)]
+
+
+@pytest.mark.parametrize("T,E,N,K", FEW)
+@pytest.mark.parametrize("kind", ["none", BF])
+def test_grouped_gated_few_rows(lib, T, E, N, K, kind):
+    """Contractions that the waves of a workgroup share unevenly (a wave's part may be empty), a row, 16 and more."""
+    K = -(-K // 128) * 128
+    test_grouped_gated(lib, T, E, N, K, kind)
+
+
 def codes(shape, seed):
     """Every finite code of e4m3 alike."""
     u = torch.randint(0, 256, shape, generator=gen(seed), dtype=torch.int16)
@@ -326,7 +337,8 @@ def block_reference(X, xs, W, ws, ends):
     return Y, off
 
 
-@pytest.mark.parametrize("T,E,N,K", [s if s[3] % 128 == 0 else (s[0], s[1], s[2], 384) for s in SHAPES] + [(70, 2, 128, 2176), (8, 1, 512, 4096)])
+@pytest.mark.parametrize("T,E,N,K", [s if s[3] % 128 == 0 else (s[0], s[1], s[2], 384) for s in SHAPES] +
+                         [(70, 2, 128, 2176), (8, 1, 512, 4096), (17, 3, 256, 1152), (60, 1, 128, 1408), (256, 1, 128, 128 * 9)])
 def test_block_product(lib, T, E, N, K):
     X, W = codes((T, K), T), codes((E, N, K), N)
     g = gen(3)
