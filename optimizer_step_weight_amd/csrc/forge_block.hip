@@ -36,11 +36,9 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(BlockArgs a) {
   const int64_t total = a.T * blocks, step = (int64_t)gridDim.x * (kThreads / 16);
   for (int64_t g = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; g < total; g += step) {
     const Place p = place_of(g, a.D, blocks);
-    float v[8] = {}, m = 0.0f;
+    float v[8] = {};
     if (p.n) unpack8<BF>(load_cols<BF, ODD>(a.x, p.at, p.n), v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = amax2(m, fabsf(v[i]));
-    const float scale = block_scale<Q>(max16(m));
+    const float scale = block_scale<Q>(max16(amax_bits(v)));
     if (p.n) store_codes<ODD>(static_cast<uint8_t*>(a.y) + p.at, encode8<Q>(v, scale), p.n);
     if ((threadIdx.x & 15) == 0) a.scale[g] = scale;
   }
@@ -62,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(BlockArgs a) {
 // One workgroup a square: thread (r, c) has rows r, r + 16, .. and columns 8 c .. 8 c + 7.
 template <bool BF, bool TURN>
 __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(BlockWeightArgs a) {
-  __shared__ float red[4];
+  __shared__ uint32_t red[4];
   __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 144];
   const int kb = (int)(a.K / 128), nb = (int)(a.N / 128);
   const int64_t sq = blockIdx.x, e = sq / ((int64_t)nb * kb);
@@ -72,19 +70,19 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(BlockWeightAr
   Raw8<BF> raw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) raw[i] = load8<BF>(a.W, base + (int64_t)(r0 + 16 * i) * a.K);
-  float m = 0.0f;
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float v[8];
     unpack8<BF>(raw[i], v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = amax2(m, fabsf(v[j]));
+    m = umax(m, amax_bits(v));
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = amax2(m, __shfl_xor(m, o));
+  m = max16(m);
+  m = umax(m, __shfl_xor(m, 16));
+  m = umax(m, __shfl_xor(m, 32));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
-  m = amax2(amax2(red[0], red[1]), amax2(red[2], red[3]));
+  m = umax(umax(red[0], red[1]), umax(red[2], red[3]));
   const float scale = block_scale<FORGE_Q_FP8>(m);
   if (threadIdx.x == 0) {
     a.scale[sq] = scale;

@@ -1,5 +1,5 @@
 // forge_gated.h -- what the products with a gated activation in their epilogue share: a tile's results
-// pass through LDS in fp32, and leave by rows, 8 columns a thread.
+// pass through LDS in fp32, and leave by rows.
 //
 // The activation needs gate and up of one column together and a block's scale needs 128 columns of one
 // row, while a wave of the contraction (forge_grouped.h) holds 128 x 128 of the tile.  So all four waves
@@ -24,7 +24,8 @@ struct Rounds {
     const int half = r / (16 * G);
     return half * 16 * MB + 16 * G * i + (r - half * 16 * G);
   }
-  // Chunk c (4 floats) of row r: 16 rows at one chunk fall into 16 places.
+  // Chunk c (4 floats) of row r.  16 rows at one chunk fall into 16 places (as they are written), and so do two
+  // rows at every other chunk (as 8 threads a row read them).
   static __device__ __forceinline__ unsigned char* at(unsigned char* smem, int r, int c) {
     return smem + r * ROW_BYTES + 16 * (c ^ (r & 15));
   }
@@ -38,14 +39,13 @@ struct Rounds {
         *reinterpret_cast<floatx4*>(at(smem, (wave >> 1) * 16 * G + 16 * b + (lane & 15),
                                        (wave & 1) * 4 * T::NB + 4 * j + (lane >> 4))) = tile.acc[I * G + b][j];
   }
-  // Columns 8 p .. 8 p + 7 of row r, from chunk c0 on.
-  static __device__ __forceinline__ void get(unsigned char* smem, int r, int c0, int p, float (&v)[8]) {
-    const floatx4 a = *reinterpret_cast<const floatx4*>(at(smem, r, c0 + 2 * p));
-    const floatx4 b = *reinterpret_cast<const floatx4*>(at(smem, r, c0 + 2 * p + 1));
+  // Eight columns of row r from chunk c on.
+  static __device__ __forceinline__ void get(unsigned char* smem, int r, int c, float* v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
+    for (int j = 0; j < 2; ++j) {
+      const floatx4 x = *reinterpret_cast<const floatx4*>(at(smem, r, c + j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = x[i];
     }
   }
 };
@@ -63,7 +63,7 @@ __device__ __forceinline__ void by_rounds(unsigned char* smem, const T& tile, F&
   });
 }
 
-__device__ __forceinline__ u32x4 to_bf16x8(const float (&v)[8]) {
+__device__ __forceinline__ u32x4 to_bf16x8(const float* v) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
 

@@ -84,6 +84,7 @@ __device__ __forceinline__ void gated_dgrad_out(const GatedDgradArgs& a, const R
                                                 int64_t n0) {
   using K = KeptRounds<HEIGHT, WIDTH, KEEP == FORGE_KEEP_BF16 ? 2 : 1>;
   constexpr int LANES = 8 * WIDTH, PER = THREADS / LANES;
+  static_assert(K::ROWS % (2 * PER) == 0, "whole passes");
   const int p = (int)threadIdx.x % LANES, lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
   const int64_t n = n0 + 8 * p;
   const bool none = t.e == a.E;  // rows of no group
@@ -110,34 +111,43 @@ __device__ __forceinline__ void gated_dgrad_out(const GatedDgradArgs& a, const R
     else wait_vm<0>();
     __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));  // LDS
     barrier();
+    // two passes over the threads at a time, or their waits for LDS and the exponentials would be in the open
+    by_act(a.act, [&](auto act) {
 #pragma unroll 1
-    for (int r = (int)threadIdx.x / LANES; r < K::ROWS; r += PER) {
-      const int tr = K::tile_row(round, r);
-      float g[8], u[8], h[8];
-      kept.template get<KEEP>(smem, round, 0, r, p, g);
-      kept.template get<KEEP>(smem, round, 1, r, p, u);
-      const floatx4 d0 = *chunk(r, 2 * p), d1 = *chunk(r, 2 * p + 1);
-      by_act(a.act, [&](auto act) {
+      for (int r = (int)threadIdx.x / LANES; r < K::ROWS; r += 2 * PER) {
+        float g[2][8], u[2][8], h[2][8], d[2][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = j < 4 ? d0[j] : d1[j - 4];
-          float v, s;
-          act_pair<decltype(act)::value>(g[j], v, s);
-          h[j] = v * u[j];
-          g[j] = d * u[j] * s;
-          u[j] = d * v;
+        for (int i = 0; i < 2; ++i) {
+          const int ri = r + PER * i;
+          kept.template get<KEEP>(smem, round, 0, ri, p, g[i]);
+          kept.template get<KEEP>(smem, round, 1, ri, p, u[i]);
+          const floatx4 d0 = *chunk(ri, 2 * p), d1 = *chunk(ri, 2 * p + 1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[i][j] = j < 4 ? d0[j] : d1[j - 4];
         }
-      });
-      if (tr >= t.rows) continue;
-      if (none)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = u[j] = h[j] = 0.0f;
-      const int64_t row = t.row0 + tr;
-      uint16_t* o = a.dGU + row * 2 * a.N + n;
-      st16_stream(o, to_bf16x8(g));
-      st16_stream(o + a.N, to_bf16x8(u));
-      if (a.H) st16_stream(a.H + row * a.N + n, to_bf16x8(h));
-    }
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float v, s;
+            act_pair<decltype(act)::value>(g[i][j], v, s);
+            h[i][j] = v * u[i][j];
+            g[i][j] = d[i][j] * u[i][j] * s;
+            u[i][j] = d[i][j] * v;
+          }
+          const int tr = K::tile_row(round, r + PER * i);
+          if (tr >= t.rows) continue;
+          if (none)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[i][j] = u[i][j] = h[i][j] = 0.0f;
+          const int64_t row = t.row0 + tr;
+          uint16_t* o = a.dGU + row * 2 * a.N + n;
+          st16_stream(o, to_bf16x8(g[i]));
+          st16_stream(o + a.N, to_bf16x8(u[i]));
+          if (a.H) st16_stream(a.H + row * a.N + n, to_bf16x8(h[i]));
+        }
+      }
+    });
     barrier();  // the round's rows have been read (their values are in registers, in order)
   }
 }

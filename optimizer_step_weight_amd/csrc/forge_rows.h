@@ -145,31 +145,59 @@ __device__ __forceinline__ float amax2(float a, float b) { return (a > b || a !=
 // most is 448 (e4m3) or 127 (int8).  The product is at most 1.5 steps of fp32 above `most`, which
 // either rounding takes back to it.  A block that holds NaN or an infinity gets a NaN scale and zero
 // codes: all of it reads back as NaN.
+//
+// Magnitudes are compared as bits, where NaN is above infinity and that above all else.  The quotients are
+// the divisions' own, in 3 operations each: a product with the inverse, corrected by its remainder (compared
+// with the division for every fp32 amax of either `most`, and every scale up to 2^121).
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int N>
+__device__ __forceinline__ uint32_t amax_bits(const float (&v)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = umax(m, mag_bits(v[i]));
+  return m;
+}
 template <int Q>
-__device__ __forceinline__ float block_scale(float amax) {
-  if (!(amax <= 3.4028234663852886e38f)) return __uint_as_float(0x7FC00000u);
-  const float s = amax / (Q == FORGE_Q_FP8 ? kFp8Max : 127.0f);
+__device__ __forceinline__ float block_scale(uint32_t amax) {
+  if (amax >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  constexpr float most = Q == FORGE_Q_FP8 ? kFp8Max : 127.0f, inv = 1.0f / most;
+  const float x = __uint_as_float(amax), q = x * inv, s = __builtin_fmaf(__builtin_fmaf(-q, most, x), inv, q);
   return s < kScaleMin ? kScaleMin : s;
+}
+__device__ __forceinline__ float inverse(float scale) {
+  const float y = __builtin_amdgcn_rcpf(scale);
+  return __builtin_fmaf(__builtin_fmaf(-scale, y, 1.0f), y, y);
+}
+// Codes of 4 values, by the inverse of their scale.
+template <int Q>
+__device__ __forceinline__ uint32_t encode4(const float* v, float inv) {
+  if constexpr (Q == FORGE_Q_FP8) {
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, w, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
+  } else {
+    // x + 1.5 * 2^23 rounds x to a whole number, whose low byte is the sum's
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[i] * inv + 12582912.0f);
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
+    return lo | hi;
+  }
+}
+// Codes of N values by their block's scale.
+template <int Q, int N>
+__device__ __forceinline__ void encode(const float (&v)[N], float scale, uint32_t (&q)[N / 4]) {
+  const float inv = inverse(scale);
+  const bool bad = scale != scale;
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) q[j] = bad ? 0u : encode4<Q>(v + 4 * j, inv);
 }
 template <int Q>
 __device__ __forceinline__ u32x2 encode8(const float (&v)[8], float scale) {
-  const float inv = 1.0f / scale;
-  u32x2 q;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if constexpr (Q == FORGE_Q_FP8) {
-      int w = 0;
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j] * inv, v[4 * j + 1] * inv, w, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j + 2] * inv, v[4 * j + 3] * inv, w, true);
-      q[j] = (uint32_t)w;
-    } else {
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)rintf(v[4 * j + i] * inv) & 0xFFu) << (8 * i);
-      q[j] = w;
-    }
-  }
-  return scale != scale ? u32x2{0, 0} : q;
+  uint32_t q[2];
+  encode<Q>(v, scale, q);
+  return u32x2{q[0], q[1]};
 }
 template <int Q>
 __device__ __forceinline__ void decode8(u32x2 q, float scale, float (&v)[8]) {
@@ -210,14 +238,15 @@ __device__ __forceinline__ void store_codes(uint8_t* p, u32x2 q, int n) {
       if (j < n) p[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
   }
 }
-// The largest over each 16 consecutive lanes, in all of them.
-__device__ __forceinline__ float max16(float v) {
-  auto join = [&](int w) { v = amax2(v, __int_as_float(w)); };
-  join(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, false));  // rotations by 8, 4, 2, 1
-  join(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, false));
-  join(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xf, 0xf, false));
-  join(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xf, 0xf, false));
-  return v;
+// The largest over each 8, or 16, consecutive lanes, in all of them.
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, false));   // 1 0 3 2 of each four
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, false));   // 2 3 0 1
+  return umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));  // 7 .. 0 of each eight
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max8(v);
+  return umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false));  // 15 .. 0 of each sixteen
 }
 
 }  // namespace forge
