@@ -22,25 +22,29 @@ namespace grp {
 
 typedef int intx8 __attribute__((ext_vector_type(8)));
 
-constexpr int BLOCK_THREADS = 512;
-constexpr int PANEL_LDS = 32768, STAGE_LDS = 2 * PANEL_LDS;   // of 256 rows of 128 bytes; X and W
-constexpr int CHUNK = 8;                                       // slabs whose scales are loaded at once
-constexpr int SCALES_AT = 2 * STAGE_LDS, SCALES_LDS = (CHUNK * 256 + 2 * CHUNK) * 4;
+constexpr int BLOCK_THREADS = 512, BLOCK_ROWS = 224;           // of a whole tile
+// LDS: three slabs of X, two of W, the scales of two chunks of 4 slabs of X and of one of 64 of W, and a place
+// for copies of nothing.
+constexpr int X_SLAB = BLOCK_ROWS * 128, W_SLAB = 256 * 128;
+constexpr int W_AT = 3 * X_SLAB, XS_AT = W_AT + 2 * W_SLAB, XS_CHUNK = 4096, WS_AT = XS_AT + 2 * XS_CHUNK;
+constexpr int WS_SLABS = 64, DUMP_AT = WS_AT + 2 * WS_SLABS * 4, BLOCK_LDS = DUMP_AT + 1024;
+static_assert(BLOCK_LDS <= 5 * 32768, "LDS");
 
 __device__ __forceinline__ int block_swz(int row) { return (row >> 1) & 7; }
 
-template <int HEIGHT, int WIDTH>  // of the tile, in 64s
+// FOURS: four scales of a row of X lie on 16 bytes, and are copied at once.
+template <int HEIGHT, int WIDTH, bool FOURS>  // of the tile, in 64s (4 rows: 224)
 __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile& t, unsigned char* smem) {
-  constexpr int MB = 2 * HEIGHT, NB = WIDTH;   // blocks of 16 rows and columns of a wave (2 x 4 waves)
-  constexpr int DX = HEIGHT, DW = WIDTH;       // copies of 1 KiB of a wave a slab
+  constexpr int MB = HEIGHT == 4 ? 7 : 2 * HEIGHT, NB = WIDTH;  // blocks of 16 rows and columns of a wave (2 x 4 waves)
+  constexpr int DX = HEIGHT, DW = WIDTH;                        // copies of 1 KiB of a wave a slab
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wr = wave >> 2, wc = wave & 3;
   const int64_t n0 = (int64_t)t.n * t.cols;
   const int KB = (int)(a.K / 128), slabs = t.e < a.E ? KB : 0;
-  const uint32_t ld = (uint32_t)a.K;
+  const uint32_t ld = (uint32_t)a.K, lds = lds_address(smem);
   const u32x4 rx = make_rsrc(a.X + (int64_t)t.row0 * a.K, (uint32_t)t.rows * ld);
   const u32x4 rw = make_rsrc(a.W + ((int64_t)t.e * a.N + n0) * a.K, (uint32_t)(64 * WIDTH) * ld);
-  const uint32_t lds = lds_address(smem);
+  const u32x4 rs = make_rsrc(a.x_scale + (int64_t)t.row0 * KB, (uint32_t)(t.rows * KB * 4));
   uint32_t ox[DX], ow[DW];  // this lane's pieces of the wave's copies
   auto piece_of = [&](int copy) {
     const int r = 8 * copy + (lane >> 3);
@@ -50,30 +54,40 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
   for (int j = 0; j < DX; ++j) ox[j] = piece_of(DX * wave + j);
 #pragma unroll
   for (int j = 0; j < DW; ++j) ow[j] = piece_of(DW * wave + j);
-  auto copy = [&](int s) {
-    const uint32_t at = lds + (uint32_t)((s & 1) * STAGE_LDS), k = (uint32_t)s * 128u;
-    static_for<DX>([&](auto j) { copy_1k<j * 1024>(rx, ox[j] + k, at + (uint32_t)(wave * DX * 1024)); });
-    static_for<DW>([&](auto j) { copy_1k<PANEL_LDS + j * 1024>(rw, ow[j] + k, at + (uint32_t)(wave * DW * 1024)); });
+  // wave 7 of a whole tile has no rows of X: its copies are of rows behind the tile's, to a place that nobody reads
+  const bool idle = HEIGHT == 4 && wave == 7;
+  const uint32_t to_x = lds + (uint32_t)(idle ? DUMP_AT - 3 * 1024 : wave * DX * 1024);
+  auto copy_x = [&](int s, uint32_t slot) {
+    const uint32_t at = idle ? to_x : to_x + slot, k = idle ? 0x80000000u : (uint32_t)s * 128u;
+    static_for<DX>([&](auto j) { copy_1k<j * 1024>(rx, ox[j] + k, idle ? lds + DUMP_AT - j * 1024 : at); });
   };
-  // Scales: two threads a row of X, four slabs each; 2 x 8 threads those of W.
-  auto scales = [&](int chunk) { return reinterpret_cast<float*>(smem + SCALES_AT + (chunk & 1) * SCALES_LDS); };
-  const int sr = (int)threadIdx.x >> 1, sh = ((int)threadIdx.x & 1) * (CHUNK / 2);
-  float sx[CHUNK / 2], sw;
-  auto fetch_scales = [&](int chunk) {
-    const int s0 = chunk * CHUNK;
+  auto copy_w = [&](int s) {
+    const uint32_t at = lds + (uint32_t)(W_AT + (s & 1) * W_SLAB + wave * DW * 1024), k = (uint32_t)s * 128u;
+    static_for<DW>([&](auto j) { copy_1k<j * 1024>(rw, ow[j] + k, at); });
+  };
+  // Scales of X of slabs 4 c .. 4 c + 3, to [row][slab] (FOURS) or [slab][row].
+  auto copy_scales = [&](int c) {
+    const uint32_t at = lds + (uint32_t)(XS_AT + (c & 1) * XS_CHUNK);
+    if constexpr (FOURS) {
+      const int r = 64 * wave + lane;  // rows from 256 on: behind the tile
+      copy_1k<0>(rs, (uint32_t)(r * KB + 4 * c) * 4u, wave < 4 ? at + (uint32_t)(wave * 1024) : lds + DUMP_AT);
+    } else {
 #pragma unroll
-    for (int j = 0; j < CHUNK / 2; ++j) {
-      const int s = s0 + sh + j;
-      sx[j] = sr < t.rows && s < slabs ? a.x_scale[(int64_t)(t.row0 + sr) * KB + s] : 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        const int g = 2 * wave + i, s = 4 * c + (g >> 2), r = 64 * (g & 3) + lane;
+        const uint32_t o = s < KB ? (uint32_t)(r * KB + s) * 4u : 0xFFFFFFF0u;
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at + (uint32_t)(g * 256)), "v"(o), "s"(rs)
+                     : "memory", "m0");
+      }
     }
-    const int s = s0 + ((int)threadIdx.x & (CHUNK - 1)), b = WIDTH == 4 ? ((int)threadIdx.x / CHUNK) & 1 : 0;
-    sw = s < slabs ? a.w_scale[((int64_t)t.e * (a.N / 128) + n0 / 128 + b) * KB + s] : 0.0f;
   };
-  auto put_scales = [&](int chunk) {
-    float* p = scales(chunk);
-#pragma unroll
-    for (int j = 0; j < CHUNK / 2; ++j) p[(sh + j) * 256 + sr] = sx[j];
-    if (threadIdx.x < 2 * CHUNK) p[CHUNK * 256 + threadIdx.x] = sw;
+  const int row = lane & 15, q = lane >> 4;
+  const float* xs = reinterpret_cast<const float*>(smem + XS_AT) + (wr * 16 * MB + row) * (FOURS ? 4 : 1);
+  float* ws = reinterpret_cast<float*>(smem + WS_AT);
+  // Scales of W of slabs s0 .. s0 + 63.
+  auto fetch_w_scales = [&](int s0) {
+    const int b = (int)threadIdx.x / WS_SLABS, s = s0 + (int)threadIdx.x % WS_SLABS;
+    if (b < WIDTH / 2) ws[threadIdx.x] = s < KB ? a.w_scale[((int64_t)t.e * (a.N / 128) + n0 / 128 + b) * KB + s] : 0.0f;
   };
 
   floatx4 acc[MB][NB];
@@ -81,60 +95,105 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{};
-  if (slabs > 0) {
-    copy(0);
-    fetch_scales(0);
-    put_scales(0);
-  }
   // addresses of a lane's two pieces: the row's swizzle is the same in every block of 16
-  const int row = lane & 15, q = lane >> 4;
   const uint32_t piece0 = (uint32_t)(row * 128 + 16 * ((2 * q) ^ block_swz(row)));
   const uint32_t piece1 = (uint32_t)(row * 128 + 16 * ((2 * q + 1) ^ block_swz(row)));
   using P4 = __attribute__((address_space(3))) const u32x4*;
-  auto frag = [&](uint32_t p0, uint32_t p1, int block) {
-    const u32x4 lo = *(P4)(p0 + block * 2048), hi = *(P4)(p1 + block * 2048);
-    return __builtin_bit_cast(intx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  struct Frag {
+    u32x4 lo, hi;
+    __device__ __forceinline__ intx8 whole() const { return __builtin_bit_cast(intx8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)); }
   };
-  for (int s = 0; s < slabs; ++s) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (s + 1 < slabs) copy(s + 1);
-    const int c = s & (CHUNK - 1);
-    if (c == 0) fetch_scales(s / CHUNK + 1);
-    const float* sc = scales(s / CHUNK);
-    const uint32_t px = lds + (uint32_t)((s & 1) * STAGE_LDS + wr * MB * 2048);
-    const uint32_t pw = lds + (uint32_t)((s & 1) * STAGE_LDS + PANEL_LDS + wc * NB * 2048);
-    const uint32_t x0 = px + piece0, x1 = px + piece1, w0 = pw + piece0, w1 = pw + piece1;
-    intx8 w[NB], x[2];
+  const uint32_t x_at = lds + (uint32_t)(wr * MB * 2048), w_at = lds + (uint32_t)(W_AT + wc * NB * 2048);
+  auto read = [&](Frag& f, uint32_t panel, int block, int half) {
+    if (half == 0) f.lo = *(P4)(panel + piece0 + block * 2048);
+    else f.hi = *(P4)(panel + piece1 + block * 2048);
+  };
+  // A product's result is added N_LATE products later, the last ones' in the next slab.
+  constexpr int BLOCKS = MB * NB, N_LATE = NB == 4 ? 3 : 1;
+  floatx4 part[N_LATE + 1];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) w[j] = frag(w0, w1, j);
-    x[0] = frag(x0, x1, 0);
-    const float w_scale = sc[CHUNK * 256 + (WIDTH == 4 ? (wc >> 1) * CHUNK : 0) + c];
-    float scale[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) scale[i] = sc[c * 256 + wr * 16 * MB + 16 * i + row];
-    __builtin_amdgcn_sched_barrier(0);
-    floatx4 part[2][NB];
-    auto add = [&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      const float f = scale[i] * w_scale;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[i & 1][j][r], f, acc[i][j][r]);
-        asm volatile("" : "+v"(acc[i][j]));  // here, not after all the products: their results would not fit
+  for (int i = 0; i <= N_LATE; ++i) part[i] = floatx4{};
+  float factor[2] = {0.0f, 0.0f};  // of the present and the last block of rows
+  Frag x[2];
+  uint32_t slot = 0;  // of slab s in the ring of X
+  // Slab s, whose W is in w; then that of slab s + 1 is in next, and its first rows of X are read.
+  // MID products in, slab s + 1 has landed for all waves (barrier), none of which needs slab s - 1 or W in LDS any
+  // more: slab s + 2 is copied there, and W of slab s + 1 read.
+  auto step = [&](auto pc, Frag (&w)[NB], Frag (&next)[NB], int s) {
+    constexpr int P = decltype(pc)::value;  // the first rows of X are in x[P]
+    constexpr int MID = 2 * NB < BLOCKS - 4 ? 2 * NB : BLOCKS / 2;
+    const float w_scale = ws[(WIDTH == 4 ? (wc >> 1) * WS_SLABS : 0) + s % WS_SLABS];
+    const float* sc = xs + ((s >> 2) & 1) * (XS_CHUNK / 4) + (s & 3) * (FOURS ? 1 : 256);
+    const uint32_t px = x_at + slot, after = slot == 2 * X_SLAB ? 0 : slot + X_SLAB;
+    const uint32_t px1 = x_at + after, pw1 = w_at + (uint32_t)(((s + 1) & 1) * W_SLAB);
+    const bool more = s + 2 < slabs;
+    float scale = sc[0];
+    static_for<BLOCKS>([&](auto nc) {
+      constexpr int n = decltype(nc)::value, i = n / NB, j = n % NB;
+      if constexpr (n == MID) {
+        wait_vm<0>();
+        barrier();
+        if ((s & 3) == 0 && s + 4 < slabs) copy_scales(s / 4 + 1);
+        if (more) copy_x(s + 2, slot == 0 ? 2 * X_SLAB : slot - X_SLAB);
+        if (more) copy_w(s + 2);
+        if ((s + 1) % WS_SLABS == 0) {
+          fetch_w_scales(s + 1);
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
       }
-    };
-    static_for<MB>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      if constexpr (i + 1 < MB) x[(i + 1) & 1] = frag(x0, x1, i + 1);
+      // the next rows of X, two pieces a block of rows
+      if constexpr (j < 2) read(x[(i + 1 + P) & 1], i + 1 < MB ? px : px1, (i + 1) % MB, j);
+      // pieces of W of the next slab, evenly over what is left
+      constexpr int FROM = MID, LEFT = BLOCKS - FROM;
+      constexpr int p0 = n < FROM ? 0 : 2 * NB * (n - FROM) / LEFT, p1 = n < FROM ? 0 : 2 * NB * (n + 1 - FROM) / LEFT;
+      static_for<p1 - p0>([&](auto k) { read(next[(p0 + decltype(k)::value) / 2], pw1, (p0 + decltype(k)::value) / 2, (p0 + decltype(k)::value) % 2); });
+      if constexpr (j == 0) {
+        factor[1] = factor[0];
+        factor[0] = scale * w_scale;
+        if constexpr (i + 1 < MB) scale = sc[16 * (i + 1) * (FOURS ? 4 : 1)];
+      }
+      part[n % (N_LATE + 1)] =
+          __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j].whole(), x[(i + P) & 1].whole(), floatx4{}, 0, 0, 0, 0, 0, 0);
+      constexpr int m = (n - N_LATE + BLOCKS) % BLOCKS;  // the block whose result is added
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        part[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j], x[i & 1], floatx4{}, 0, 0, 0, 0, 0, 0);
-      if constexpr (i > 0) add(std::integral_constant<int, i - 1>{});
+      for (int r = 0; r < 4; ++r)
+        acc[m / NB][m % NB][r] = __builtin_fmaf(part[(n + 1) % (N_LATE + 1)][r], factor[j < N_LATE ? 1 : 0], acc[m / NB][m % NB][r]);
+      asm volatile("" : "+v"(acc[m / NB][m % NB]));  // here, not after all the products
       __builtin_amdgcn_sched_barrier(0);
     });
-    add(std::integral_constant<int, MB - 1>{});
-    if (c == CHUNK - 1) put_scales(s / CHUNK + 1);
+    slot = after;
+  };
+  if (slabs > 0) {
+    fetch_w_scales(0);
+    copy_scales(0);
+    copy_x(0, 0);
+    copy_w(0);
+    if (slabs > 1) {
+      copy_x(1, X_SLAB);
+      copy_w(1);
+      wait_vm<DX + DW>();
+    } else {
+      wait_vm<0>();
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    Frag wa[NB], wb[NB];
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) read(wa[j / 2], w_at, j / 2, j % 2);
+    read(x[0], x_at, 0, 0);
+    read(x[0], x_at, 0, 1);
+    for (int s = 0; s < slabs; s += 2) {
+      step(std::integral_constant<int, 0>{}, wa, wb, s);
+      if (s + 1 < slabs) step(std::integral_constant<int, MB & 1>{}, wb, wa, s + 1);
+    }
+    // the last products' results
+#pragma unroll
+    for (int k = 0; k < N_LATE; ++k) {
+      constexpr int at = BLOCKS - N_LATE;
+      const int m = at + k;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[m / NB][m % NB][r] = __builtin_fmaf(part[m % (N_LATE + 1)][r], factor[0], acc[m / NB][m % NB][r]);
+    }
   }
   __syncthreads();
   // out by rows through LDS in bf16: 16-byte chunks are XOR-swizzled with the row
@@ -154,20 +213,21 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
   }
 }
 
+template <bool FOURS>
 __global__ __launch_bounds__(BLOCK_THREADS, 2) void block_gemm_kernel(BlockGemmArgs a) {
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[SCALES_AT + 2 * SCALES_LDS];
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[BLOCK_LDS];
   RowTile t;
-  if (!find_tile<256>(a.ends, a.E, a.T, a.N, a.cols, (int)blockIdx.x, t)) return;
+  if (!find_tile<BLOCK_ROWS>(a.ends, a.E, a.T, a.N, a.cols, (int)blockIdx.x, t)) return;
   const bool narrow = t.cols < 256 || a.N - (int64_t)t.n * 256 < 256;
   switch ((t.rows + 63) / 64 + (narrow ? 4 : 0)) {
-    case 1: block_tile<1, 4>(a, t, smem); break;
-    case 2: block_tile<2, 4>(a, t, smem); break;
-    case 3: block_tile<3, 4>(a, t, smem); break;
-    case 4: block_tile<4, 4>(a, t, smem); break;
-    case 5: block_tile<1, 2>(a, t, smem); break;
-    case 6: block_tile<2, 2>(a, t, smem); break;
-    case 7: block_tile<3, 2>(a, t, smem); break;
-    case 8: block_tile<4, 2>(a, t, smem); break;
+    case 1: block_tile<1, 4, FOURS>(a, t, smem); break;
+    case 2: block_tile<2, 4, FOURS>(a, t, smem); break;
+    case 3: block_tile<3, 4, FOURS>(a, t, smem); break;
+    case 4: block_tile<4, 4, FOURS>(a, t, smem); break;
+    case 5: block_tile<1, 2, FOURS>(a, t, smem); break;
+    case 6: block_tile<2, 2, FOURS>(a, t, smem); break;
+    case 7: block_tile<3, 2, FOURS>(a, t, smem); break;
+    case 8: block_tile<4, 2, FOURS>(a, t, smem); break;
   }
 }
 
@@ -176,10 +236,13 @@ __global__ __launch_bounds__(BLOCK_THREADS, 2) void block_gemm_kernel(BlockGemmA
 int launch_grouped_block_gemm(const BlockGemmArgs& given, void* stream) {
   if (few_rows_call(given.T, given.E, given.N, 128)) return launch_block_few(given, stream);
   BlockGemmArgs a = given;
-  const int64_t row_tiles = a.T / 256 + (a.E < a.T ? a.E : a.T) + 1;
-  a.cols = a.T / 256 * ((a.N + 255) / 256) <= grp::NARROW_TILES ? 128 : 256;  // as launch_grouped_rows
+  const int64_t row_tiles = a.T / grp::BLOCK_ROWS + (a.E < a.T ? a.E : a.T) + 1;
+  a.cols = a.T / grp::BLOCK_ROWS * ((a.N + 255) / 256) <= grp::NARROW_TILES ? 128 : 256;  // as launch_grouped_rows
   const int64_t tiles = row_tiles * ((a.N + a.cols - 1) / a.cols);
-  hipLaunchKernelGGL(grp::block_gemm_kernel, dim3((unsigned)tiles), dim3(grp::BLOCK_THREADS), 0, (hipStream_t)stream, a);
+  // four scales of X on 16 bytes: a row's begin there too, and so does the tensor
+  const bool fours = a.K % 512 == 0 && (reinterpret_cast<uintptr_t>(a.x_scale) & 15) == 0;
+  hipLaunchKernelGGL((fours ? grp::block_gemm_kernel<true> : grp::block_gemm_kernel<false>), dim3((unsigned)tiles),
+                     dim3(grp::BLOCK_THREADS), 0, (hipStream_t)stream, a);
   return (int)hipGetLastError();
 }
 
