@@ -56,15 +56,15 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
   for (int j = 0; j < DW; ++j) ow[j] = piece_of(DW * wave + j);
   // wave 7 of a whole tile has no rows of X: its copies are of rows behind the tile's, to a place that nobody reads
   const bool idle = HEIGHT == 4 && wave == 7;
-  const uint32_t to_x = lds + (uint32_t)(idle ? DUMP_AT - 3 * 1024 : wave * DX * 1024);
-  auto copy_x = [&](int s, uint32_t slot) {
-    const uint32_t at = idle ? to_x : to_x + slot, k = idle ? 0x80000000u : (uint32_t)s * 128u;
-    static_for<DX>([&](auto j) { copy_1k<j * 1024>(rx, ox[j] + k, idle ? lds + DUMP_AT - j * 1024 : at); });
+  // Copy j of slab s; of slabs behind the last, nothing (past the operand's end: zeros, which nobody reads).
+  auto copy_x = [&](auto j, uint32_t k, uint32_t slot) {
+    copy_1k<j * 1024>(rx, ox[j] + k, idle ? lds + DUMP_AT - j * 1024 : lds + slot + (uint32_t)(wave * DX * 1024));
   };
-  auto copy_w = [&](int s) {
-    const uint32_t at = lds + (uint32_t)(W_AT + (s & 1) * W_SLAB + wave * DW * 1024), k = (uint32_t)s * 128u;
-    static_for<DW>([&](auto j) { copy_1k<j * 1024>(rw, ow[j] + k, at); });
+  auto copy_w = [&](auto j, uint32_t k, int s) {
+    copy_1k<j * 1024>(rw, ow[j] + k, lds + (uint32_t)(W_AT + (s & 1) * W_SLAB + wave * DW * 1024));
   };
+  auto place = [&](int s) { return s < slabs ? (uint32_t)s * 128u : 0x80000000u; };
+  const uint32_t skip = idle ? 0x80000000u : 0u;
   // Scales of X of slabs 4 c .. 4 c + 3, to [row][slab] (FOURS) or [slab][row].
   auto copy_scales = [&](int c) {
     const uint32_t at = lds + (uint32_t)(XS_AT + (c & 1) * XS_CHUNK);
@@ -126,7 +126,7 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
     const float* sc = xs + ((s >> 2) & 1) * (XS_CHUNK / 4) + (s & 3) * (FOURS ? 1 : 256);
     const uint32_t px = x_at + slot, after = slot == 2 * X_SLAB ? 0 : slot + X_SLAB;
     const uint32_t px1 = x_at + after, pw1 = w_at + (uint32_t)(((s + 1) & 1) * W_SLAB);
-    const bool more = s + 2 < slabs;
+    const uint32_t k2 = place(s + 2), slot2 = slot == 0 ? 2 * X_SLAB : slot - X_SLAB;
     float scale = sc[0];
     static_for<BLOCKS>([&](auto nc) {
       constexpr int n = decltype(nc)::value, i = n / NB, j = n % NB;
@@ -134,12 +134,19 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
         wait_vm<0>();
         barrier();
         if ((s & 3) == 0 && s + 4 < slabs) copy_scales(s / 4 + 1);
-        if (more) copy_x(s + 2, slot == 0 ? 2 * X_SLAB : slot - X_SLAB);
-        if (more) copy_w(s + 2);
         if ((s + 1) % WS_SLABS == 0) {
           fetch_w_scales(s + 1);
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
+      }
+      // slab s + 2, at an even pace: in a burst the waves wait for each other to issue their copies
+      if constexpr (n >= MID) {
+        constexpr int c0 = (DX + DW) * (n - MID) / (BLOCKS - MID), c1 = (DX + DW) * (n + 1 - MID) / (BLOCKS - MID);
+        static_for<c1 - c0>([&](auto k) {
+          constexpr int c = c0 + decltype(k)::value;
+          if constexpr (c < DX) copy_x(std::integral_constant<int, c>{}, k2 | skip, slot2);
+          else copy_w(std::integral_constant<int, c - DX>{}, k2, s);
+        });
       }
       // the next rows of X, two pieces a block of rows
       if constexpr (j < 2) read(x[(i + 1 + P) & 1], i + 1 < MB ? px : px1, (i + 1) % MB, j);
@@ -166,15 +173,12 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
   if (slabs > 0) {
     fetch_w_scales(0);
     copy_scales(0);
-    copy_x(0, 0);
-    copy_w(0);
-    if (slabs > 1) {
-      copy_x(1, X_SLAB);
-      copy_w(1);
-      wait_vm<DX + DW>();
-    } else {
-      wait_vm<0>();
-    }
+    static_for<2>([&](auto sc) {
+      constexpr int s = decltype(sc)::value;
+      static_for<DX>([&](auto j) { copy_x(j, place(s) | skip, s * X_SLAB); });
+      static_for<DW>([&](auto j) { copy_w(j, place(s), s); });
+    });
+    wait_vm<DX + DW>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     Frag wa[NB], wb[NB];
 #pragma unroll
@@ -185,6 +189,7 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
       step(std::integral_constant<int, 0>{}, wa, wb, s);
       if (s + 1 < slabs) step(std::integral_constant<int, MB & 1>{}, wb, wa, s + 1);
     }
+    wait_vm<0>();  // no copy may land in what LDS takes next
     // the last products' results
 #pragma unroll
     for (int k = 0; k < N_LATE; ++k) {
