@@ -1,5 +1,6 @@
 """PyTorch autograd integration: layers whose backward pass updates their own weight (`FusedLinear`,
-and `FusedExperts` over the experts of a mixture), and the RMS norm before them (`RMSNorm`).
+`FusedExperts` over the experts of a mixture, and `FusedGatedExperts`, a gated feed-forward block of two
+such layers), and the RMS norm before them (`RMSNorm`).
 
 FORGE explainer (gist.science), Technical Summary section 2 "Core Mechanism": the weight
 gradient of a layer is consumed tile by tile by the optimizer and never stored.  In a PyTorch
@@ -14,6 +15,9 @@ embeddings, shared layers) cannot be updated by one of them, and non-element-wis
 global gradient-norm clipping cannot see this weight's gradient.  Each forward of a layer must be
 followed by exactly one backward before the next forward.
 
+Layers take `checkpoint`: "int8" or "fp8" keeps what their backward pass needs of the activations in 8
+bits, in blocks of 128 columns with a scale each, instead of whole.
+
 All arithmetic runs in the library's kernels; this module only marshals tensors.
 """
 from __future__ import annotations
@@ -22,8 +26,8 @@ from typing import Optional
 
 import torch
 
-from . import (grouped_dgrad, grouped_gemm, grouped_wgrad_step, linear_backward_step, rmsnorm, rmsnorm_backward,
-               wgrad_step)
+from . import (block_dequantize, block_quantize, grouped_dgrad, grouped_gated, grouped_gated_dgrad, grouped_gemm,
+               grouped_wgrad_step, linear_backward_step, rmsnorm, rmsnorm_backward, wgrad_step)
 
 _STATES = {"adamw": "mv", "nadam": "mv", "radam": "mv", "lion": "m", "rmsprop": "v", "adagrad": "v",
            "sgd": "", "sgd_momentum": "m"}
@@ -36,16 +40,45 @@ def _packed(t: torch.Tensor) -> torch.Tensor:
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+_CODES = {"int8": torch.int8, "fp8": torch.float8_e4m3fn}
+
+
+def _checkpoint(how):
+    """The type of the codes that activations are kept in, or None."""
+    if how is not None and how not in _CODES:
+        raise ValueError(f"checkpoint must be None, 'int8' or 'fp8' (got {how!r})")
+    return None if how is None else _CODES[how]
+
+
+def _keep(x2d: torch.Tensor, codes):
+    """x2d as it is kept for the backward pass: itself, or its codes and their scales."""
+    if codes is None:
+        return (x2d,)
+    q = torch.empty(x2d.shape, dtype=codes, device=x2d.device)
+    scale = torch.empty(x2d.shape[0], -(-x2d.shape[1] // 128), device=x2d.device)
+    block_quantize(x2d, q, scale)
+    return q, scale
+
+
+def _kept(saved) -> torch.Tensor:
+    """What _keep was given (bfloat16), as far as its codes say."""
+    if len(saved) == 1:
+        return saved[0]
+    x2d = torch.empty(saved[0].shape, dtype=torch.bfloat16, device=saved[0].device)
+    block_dequantize(*saved, x2d)
+    return x2d
+
+
 class _LinearStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x2d, anchor, layer):
         ctx.layer = layer
-        ctx.save_for_backward(x2d)
+        ctx.save_for_backward(*_keep(x2d, layer.codes))
         return x2d @ layer.weight.t()
 
     @staticmethod
     def backward(ctx, dy):
-        (x2d,) = ctx.saved_tensors
+        x2d = _kept(ctx.saved_tensors)
         layer = ctx.layer
         dy = _packed(dy.to(layer.weight.dtype))
         layer.step_count += 1
@@ -69,12 +102,14 @@ class FusedLinear(torch.nn.Module):
         0.999, eps 1e-8, no weight decay).
     state_dtype: "f32" or "int8" (block-64 absmax moments).
     seed: the stochastic-rounding key of this layer (give every layer its own).
+    checkpoint: None, "int8" or "fp8": how the input is kept for the backward pass.
     """
 
     def __init__(self, in_features: int, out_features: int, *, opt: str = "adamw",
                  hyper=None, state_dtype: str = "f32", seed: int = 0,
-                 weight: Optional[torch.Tensor] = None, device="cuda"):
+                 weight: Optional[torch.Tensor] = None, checkpoint: Optional[str] = None, device="cuda"):
         super().__init__()
+        self.codes = _checkpoint(checkpoint)
         if in_features % 128 or out_features % 128:
             raise ValueError("in_features and out_features must be multiples of 128")
         if opt not in _STATES:
@@ -127,24 +162,29 @@ class _ExpertsStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x2d, anchor, ends, layer):
         ctx.layer = layer
-        ctx.save_for_backward(x2d, ends)
+        ctx.save_for_backward(ends, *_keep(x2d, layer.codes))
         y = torch.empty(x2d.shape[0], layer.out_features, dtype=torch.bfloat16, device=x2d.device)
         grouped_gemm(x2d, layer.weight, ends, y)
         return y
 
     @staticmethod
     def backward(ctx, dy):
-        x2d, ends = ctx.saved_tensors
+        ends, *saved = ctx.saved_tensors
+        x2d = _kept(saved)
         layer = ctx.layer
         dy = _packed(dy.to(torch.bfloat16))
-        layer.step_count += 1
         dx = None
         if ctx.needs_input_grad[0]:   # with the weights as they were
             dx = torch.empty_like(x2d)
             grouped_dgrad(dy, layer.weight, ends, dx)
-        grouped_wgrad_step(x2d, dy, ends, layer.weight, layer.m, layer.v, opt=layer.opt, hyper=layer.hyper,
-                           step=layer.step_count, seed=layer.seed, m_scale=layer.m_scale, v_scale=layer.v_scale)
+        _step_experts(layer, x2d, dy, ends)
         return dx, None, None, None
+
+
+def _step_experts(layer, x2d, dy, ends) -> None:
+    layer.step_count += 1
+    grouped_wgrad_step(x2d, dy, ends, layer.weight, layer.m, layer.v, opt=layer.opt, hyper=layer.hyper,
+                       step=layer.step_count, seed=layer.seed, m_scale=layer.m_scale, v_scale=layer.v_scale)
 
 
 class FusedExperts(FusedLinear):
@@ -155,7 +195,8 @@ class FusedExperts(FusedLinear):
     and one backward for each forward are FusedLinear's."""
 
     def __init__(self, experts: int, in_features: int, out_features: int, *, opt: str = "adamw", hyper=None,
-                 state_dtype: str = "f32", seed: int = 0, weight: Optional[torch.Tensor] = None, device="cuda"):
+                 state_dtype: str = "f32", seed: int = 0, weight: Optional[torch.Tensor] = None,
+                 checkpoint: Optional[str] = None, device="cuda"):
         if weight is not None:
             if tuple(weight.shape) != (experts, out_features, in_features):
                 raise ValueError(f"weight must be [{experts}, {out_features}, {in_features}] (got {tuple(weight.shape)})")
@@ -166,7 +207,7 @@ class FusedExperts(FusedLinear):
         if weight is None:
             weight = torch.randn(experts * out_features, in_features, device=device) * scale
         super().__init__(in_features, experts * out_features, opt=opt, hyper=hyper, state_dtype=state_dtype, seed=seed,
-                         weight=weight, device=device)
+                         weight=weight, checkpoint=checkpoint, device=device)
         self.experts, self.out_features = int(experts), out_features
         shape = (experts, out_features, in_features)
         for name in ("weight", "m", "v"):
@@ -184,32 +225,110 @@ class FusedExperts(FusedLinear):
         return f"experts={self.experts}, " + super().extra_repr()
 
 
+class _GatedStep(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x2d, anchor, ends, layer):
+        ctx.layer = layer
+        up, down, rows = layer.gate_up, layer.down, x2d.shape[0]
+        new = lambda n, dt=torch.bfloat16: torch.empty(rows, n, dtype=dt, device=x2d.device)  # noqa: E731
+        hidden, y = new(layer.hidden), new(down.out_features)
+        kept, scale = new(2 * layer.hidden, up.codes or torch.bfloat16), None
+        if up.codes is not None:
+            scale = new(2 * layer.hidden // 128, torch.float32)
+        grouped_gated(x2d, up.weight, ends, hidden, gate_up=kept, gate_up_scale=scale, act=layer.act)
+        grouped_gemm(hidden, down.weight, ends, y)   # `hidden` is not kept: the backward pass has it from gate and up
+        ctx.save_for_backward(ends, kept, scale, *_keep(x2d, up.codes))
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        ends, kept, scale, *saved = ctx.saved_tensors
+        layer = ctx.layer
+        up, down = layer.gate_up, layer.down
+        dy = _packed(dy.to(torch.bfloat16))
+        grad = torch.empty(kept.shape, dtype=torch.bfloat16, device=kept.device)
+        hidden = torch.empty(kept.shape[0], layer.hidden, dtype=torch.bfloat16, device=kept.device)
+        grouped_gated_dgrad(dy, down.weight, ends, kept, grad, H=hidden, gate_up_scale=scale, act=layer.act)
+        _step_experts(down, hidden, dy, ends)
+        del hidden
+        dx = None
+        if ctx.needs_input_grad[0]:
+            dx = torch.empty(kept.shape[0], up.in_features, dtype=torch.bfloat16, device=kept.device)
+            grouped_dgrad(grad, up.weight, ends, dx)
+        _step_experts(up, _kept(saved), grad, ends)
+        return dx, None, None, None
+
+
+class FusedGatedExperts(torch.nn.Module):
+    """y[t] = (act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)) Wd[e]^T for the rows t of expert e: a gated feed-forward
+    block whose backward pass updates its weights, those of `gate_up` [experts, 2 hidden, width] (gate
+    rows, then up rows) and of `down` [experts, width, hidden], both FusedExperts.  width and hidden are
+    multiples of 128.  act: silu, gelu, gelu_tanh or relu.  checkpoint: None, "int8" or "fp8": how gate,
+    up and the input are kept; the product of gate and up is not kept at all.  The other arguments, the limits
+    and one backward for each forward are FusedLinear's; seed goes to gate_up and seed + 1 to down.
+
+    forward(x, ends): the rows of x [rows, width] are sorted by expert, ends[e] (int32, on the device) is the
+    first row after expert e.  With one expert (a dense block) ends may be left out, and x have any leading
+    dimensions."""
+
+    def __init__(self, experts: int, width: int, hidden: int, *, act: str = "silu", opt: str = "adamw", hyper=None,
+                 state_dtype: str = "f32", seed: int = 0, checkpoint: Optional[str] = None, device="cuda"):
+        super().__init__()
+        from .ffn import _act
+        _act(act)
+        if hidden % 128:
+            raise ValueError("width and hidden must be multiples of 128")
+        kw = dict(opt=opt, hyper=hyper, state_dtype=state_dtype, checkpoint=checkpoint, device=device)
+        self.act, self.width, self.hidden = act, int(width), int(hidden)
+        self.gate_up = FusedExperts(experts, width, 2 * hidden, seed=seed, **kw)
+        self.down = FusedExperts(experts, hidden, width, seed=seed + 1, **kw)
+
+    def forward(self, x: torch.Tensor, ends: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if x.shape[-1] != self.width:
+            raise ValueError(f"expected last dimension {self.width}, got {x.shape[-1]}")
+        lead = x.shape[:-1]
+        if ends is None:
+            if self.gate_up.experts != 1:
+                raise ValueError(f"{self.gate_up.experts} experts need ends")
+            x = x.reshape(-1, self.width)
+            ends = torch.full((1,), x.shape[0], dtype=torch.int32, device=x.device)
+        elif x.dim() != 2 or ends.numel() != self.gate_up.experts:
+            raise ValueError(f"with ends [{self.gate_up.experts}], x must be [rows, {self.width}] "
+                             f"(got {ends.numel()} ends, {tuple(x.shape)})")
+        y = _GatedStep.apply(_packed(x.to(torch.bfloat16)), self.gate_up._anchor, ends, self)
+        return y.reshape(*lead, self.width)
+
+    def extra_repr(self) -> str:
+        return f"width={self.width}, hidden={self.hidden}, act={self.act}"
+
+
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, residual, gain, eps):
+    def forward(ctx, x, residual, gain, eps, codes):
         h = None if residual is None else torch.empty_like(x)
         y = torch.empty_like(x)
         rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
         rmsnorm(x, gain, y, residual=residual, h=h, rstd=rstd, eps=eps)
-        ctx.save_for_backward(x if h is None else h, gain, rstd)
+        ctx.save_for_backward(gain, rstd, *_keep(x if h is None else h, codes))
         ctx.alone = h is None
         ctx.set_materialize_grads(False)
         return y if h is None else (y, h)
 
     @staticmethod
     def backward(ctx, dy, dh=None):
-        h, gain, rstd = ctx.saved_tensors
+        gain, rstd, *h = ctx.saved_tensors
         if dy is None:   # only the stream was used
-            return dh, dh, None, None
+            return dh, dh, None, None, None
         grads = _RMSNormGrad.apply if torch.is_grad_enabled() else _norm_grads
-        dx, dgain = grads(dy, dh, h, gain, rstd, ctx.needs_input_grad[2])
-        return dx, None if ctx.alone else dx, dgain, None
+        dx, dgain = grads(dy, dh, gain, rstd, ctx.needs_input_grad[2], *h)
+        return dx, None if ctx.alone else dx, dgain, None, None
 
 
-def _norm_grads(dy, dh, h, gain, rstd, want_gain):
-    dx = torch.empty_like(h)
+def _norm_grads(dy, dh, gain, rstd, want_gain, h, scale=None):
+    dx = torch.empty(h.shape, dtype=dy.dtype, device=h.device)
     dgain = torch.empty(gain.shape, dtype=torch.float32, device=h.device) if want_gain else None
-    rmsnorm_backward(_packed(dy), h, gain, rstd, dx, dgain, dh=None if dh is None else _packed(dh))
+    rmsnorm_backward(_packed(dy), h, gain, rstd, dx, dgain, dh=None if dh is None else _packed(dh),
+                     **({} if scale is None else {"h_scale": scale}))
     return dx, None if dgain is None else dgain.to(gain.dtype)
 
 
@@ -229,11 +348,12 @@ class _RMSNormGrad(torch.autograd.Function):
 class RMSNorm(torch.nn.Module):
     """y = h / sqrt(mean(h^2) + eps) * gain over the last dimension (float32 or bfloat16), with h = x.
     With a residual of the same shape h = x + residual, rounded to their dtype, and forward returns
-    (y, h): h goes on as the residual stream.  gain is an ordinary parameter (float32).  It can be
-    differentiated once: a second derivative raises."""
+    (y, h): h goes on as the residual stream.  gain is an ordinary parameter (float32).  checkpoint: None, "int8" or
+    "fp8": how h is kept for the backward pass.  It can be differentiated once: a second derivative raises."""
 
-    def __init__(self, width: int, *, eps: float = 1e-6, device="cuda"):
+    def __init__(self, width: int, *, eps: float = 1e-6, checkpoint: Optional[str] = None, device="cuda"):
         super().__init__()
+        self.codes = _checkpoint(checkpoint)
         self.width, self.eps = int(width), float(eps)
         self.gain = torch.nn.Parameter(torch.ones(width, device=device))
 
@@ -243,7 +363,8 @@ class RMSNorm(torch.nn.Module):
         if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
             raise ValueError("residual must have the shape and dtype of x")
         flat = lambda t: _packed(t.reshape(-1, self.width))  # noqa: E731
-        out = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), _packed(self.gain), self.eps)
+        out = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), _packed(self.gain), self.eps,
+                             self.codes)
         return out.view(x.shape) if residual is None else tuple(t.view(x.shape) for t in out)
 
     def extra_repr(self) -> str:

@@ -178,3 +178,84 @@ def test_codes_are_within_half_a_step():
         top = s.to(R.F64).repeat_interleave(128, 1)[:, :300]
         step = 2.0 ** -4 * x.to(R.F64).abs() + 2.0 ** -10 * top if kind is R.FP8 else 0.5 * top
         assert bool(((R.value(q, s) - x.to(R.F64)).abs() <= step * (1 + 1e-4)).all())
+
+
+# ------------------------------------------------------------------ the layers, with stand-ins for the library
+@pytest.fixture()
+def A(monkeypatch):
+    from optimizer_step_weight_amd import autograd
+
+    def fine(*tensors):
+        for t in tensors:
+            assert t is None or (t.data_ptr() % 16 == 0 and t.is_contiguous())
+
+    def grouped_gated(X, W, ends, H, *, gate_up=None, gate_up_scale=None, act):
+        fine(X, W, H, gate_up)
+        gu, _ = R.grouped(X, W, ends, True)
+        n = H.shape[1]
+        H.copy_(R.act(act, gu[:, :n])[0] * gu[:, n:])
+        if gate_up_scale is None:
+            gate_up.copy_(gu)
+        else:
+            q, s = R.quantize(gu, gate_up.dtype)
+            gate_up.copy_(q)
+            gate_up_scale.copy_(s.view(gate_up_scale.shape))
+
+    def grouped_gated_dgrad(dY, W, ends, gate_up, dgate_up, *, H=None, gate_up_scale=None, act):
+        fine(dY, W, gate_up, dgate_up, H)
+        v = gate_up.to(R.F64) if gate_up_scale is None else R.value(gate_up, gate_up_scale)
+        n = H.shape[1]
+        (dg, du, h), _ = R.gated_grads(act, R.grouped(dY, W, ends, False)[0], v[:, :n], v[:, n:])
+        dgate_up.copy_(torch.cat([dg, du], 1))
+        H.copy_(h)
+    steps = []
+    monkeypatch.setattr(autograd, "grouped_gated", grouped_gated)
+    monkeypatch.setattr(autograd, "grouped_gated_dgrad", grouped_gated_dgrad)
+    monkeypatch.setattr(autograd, "grouped_gemm", lambda X, W, ends, Y: Y.copy_(R.grouped(X, W, ends, True)[0]))
+    monkeypatch.setattr(autograd, "grouped_dgrad", lambda X, W, ends, Y: Y.copy_(R.grouped(X, W, ends, False)[0]))
+    monkeypatch.setattr(autograd, "grouped_wgrad_step", lambda X, dY, ends, W, *a, **k: steps.append((X.clone(), dY.clone(), W, k)))
+    monkeypatch.setattr(autograd, "block_quantize", lambda x, q, s: [a.copy_(b) for a, b in zip((q, s), R.quantize(x, q.dtype))])
+    monkeypatch.setattr(autograd, "block_dequantize", lambda q, s, y: y.copy_(R.value(q, s)))
+    return autograd, steps
+
+
+@pytest.mark.parametrize("how", [None, "int8", "fp8"])
+def test_gated_layer_gradients(A, how):
+    """The input's gradient and what the weights' steps are given, against autograd in 64 bits."""
+    A, steps = A
+    T, K, N, E = 9, 128, 256, 2
+    torch.manual_seed(1)
+    layer = A.FusedGatedExperts(E, K, N, act="silu", checkpoint=how, device="cpu")
+    x, dy = torch.randn(T + 1, K)[1:].to(torch.bfloat16).requires_grad_(True), torch.randn(T, K).to(torch.bfloat16)
+    ends = torch.tensor([4, T], dtype=torch.int32)
+    layer(x, ends).backward(dy)
+    assert layer.gate_up.step_count == layer.down.step_count == 1 and [k["seed"] for *_, k in steps] == [1, 0]
+    x64 = x.detach().double().requires_grad_(True)
+    ws = [layer.gate_up.weight.detach().double().requires_grad_(True), layer.down.weight.detach().double().requires_grad_(True)]
+    out = []
+    for e, (a, b) in enumerate(((0, 4), (4, T))):
+        g, u = (x64[a:b] @ ws[0][e].t()).split(N, 1)
+        out.append((torch.nn.functional.silu(g) * u) @ ws[1][e].t())
+    torch.cat(out).backward(dy.double())
+    # relative to the largest: bf16 in several places, and codes within 1 / 254 or 1 / 16 of theirs
+    slack = {None: 0.02, "int8": 0.04, "fp8": 0.2}[how]
+    near = lambda a, b: float((a.double() - b).abs().max()) <= slack * float(b.abs().max())  # noqa: E731
+    assert near(x.grad, x64.grad)
+    for (X, dY, W, _), w in zip(steps, (ws[1], ws[0])):
+        dW = torch.stack([dY[a:b].double().t() @ X[a:b].double() for a, b in ((0, 4), (4, T))])
+        assert near(dW, w.grad)
+
+
+def test_gated_layer_arguments(A):
+    A, _ = A
+    for kw in (dict(act="swish"), dict(checkpoint="int4"), dict(hidden=200), dict(width=100)):
+        with pytest.raises(ValueError):
+            A.FusedGatedExperts(**dict(dict(experts=1, width=128, hidden=128, device="cpu"), **kw))
+    layer = A.FusedGatedExperts(2, 128, 128, device="cpu")
+    for args in ((torch.zeros(3, 64),), (torch.zeros(3, 128),), (torch.zeros(3, 128), torch.zeros(3, dtype=torch.int32)),
+                 (torch.zeros(1, 3, 128), torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            layer(*args)
+    for make in (lambda: A.FusedLinear(128, 128, checkpoint="no", device="cpu"), lambda: A.RMSNorm(8, checkpoint="no", device="cpu")):
+        with pytest.raises(ValueError, match="checkpoint"):
+            make()
