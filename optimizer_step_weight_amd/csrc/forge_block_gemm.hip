@@ -239,7 +239,7 @@ __global__ __launch_bounds__(BLOCK_THREADS, 2) void block_gemm_kernel(BlockGemmA
 }  // namespace grp
 
 int launch_grouped_block_gemm(const BlockGemmArgs& given, void* stream) {
-  if (few_rows_call(given.T, given.E, given.N, 128)) return launch_block_few(given, stream);
+  if (few_rows_call(given.T, given.E, given.N, 128, kFewBlock)) return launch_block_few(given, stream);
   BlockGemmArgs a = given;
   const int64_t row_tiles = a.T / grp::BLOCK_ROWS + (a.E < a.T ? a.E : a.T) + 1;
   a.cols = a.T / grp::BLOCK_ROWS * ((a.N + 255) / 256) <= grp::NARROW_TILES ? 128 : 256;  // as launch_grouped_rows

@@ -10,7 +10,7 @@
 // one did, and its beginning and end were not covered (block product of 14336 x 4096, one row: 22 us; 19 us now).
 //
 // One row, gated product: 4096 x 4096 15 us (4.5 TB/s), 1408 x 2048 8.5 us (tiles: 14).  Block product, 4096 x 14336: 15 us
-// for one row (3.9 TB/s), 22 us for 16; tiles: 97.
+// for one row (3.9 TB/s), 22 us for 16; tiles: 94.  (Lanes without a row could spare their loads of X: no gain.)
 #include <hip/hip_runtime.h>
 
 #include "forge_act.h"

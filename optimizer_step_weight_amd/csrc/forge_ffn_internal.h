@@ -95,15 +95,18 @@ struct BlockGemmArgs {
 int launch_grouped_block_gemm(const BlockGemmArgs& a, void* stream);
 int launch_block_few(const BlockGemmArgs& a, void* stream);
 // Whether the kernels of few rows (forge_few.hip) take a call, by the least tiles of the other kernels that its rows
-// and columns make: these are slow where they leave CUs without any, those read X again for each 16 columns.
-// In us, few rows against tiles, one weight: gated product of 4096 x 4096 (64 tiles) 17 against 43 at 16 rows, 29
-// against 42 at 64, 54 against 44 at 128; of 8192 x 2048 (128 tiles) 21 against 26 at 32 rows, 32 against 26 at 64; of
-// 14336 x 4096 (224 tiles) 49 against 46 at 1.  Block product of 4096 x 14336 (32 tiles) 22 against 97 at 16 rows, 95
-// against 142 at 128; of 14336 x 4096 (112 tiles) 35 against 42 at 32 rows, 61 against 44 at 64; of 2048 x 4096 (16 tiles)
-// 32 against 41 at 256.
-inline bool few_rows_call(int64_t T, int32_t E, int64_t N, int64_t cols) {
+// and columns make, `cols` columns each: these are slow where they leave CUs without any, those read X again for each
+// 16 columns.  In us, few rows against tiles, one weight:
+//   gated product  4096 x 4096 (64 tiles): 17 against 41 at 16 rows, 29 against 41 at 64, 54 against 44 at 128;
+//                  8192 x 2048 (128): 21 against 25 at 32 rows, 32 against 25 at 64; 1408 x 2048 (22): 10 against 14 at 16
+//                  rows, 17 against 14 at 64; 14336 x 4096 (224): 49 against 46 at one row
+//   block product  4096 x 14336 (32): 22 against 94 at 16 rows, 49 against 95 at 64, 95 against 105 at 128; 4096 x 4096 (32):
+//                  17 against 20 at 64 rows, 32 against 23 at 128; 14336 x 4096 (112): 24 against 31 at 16 rows, 35 against 31
+//                  at 32; 2048 x 4096 (16): 17 against 23 at 128 rows, 32 against 29 at 256
+inline bool few_rows_call(int64_t T, int32_t E, int64_t N, int64_t cols, int64_t most) {
   const int64_t tiles = (E < T ? E : T) * (N / cols);
-  return T <= 256 && tiles <= 128 && T * tiles <= 4096;
+  return T <= 256 && tiles <= 128 && T * tiles <= most;
 }
+constexpr int64_t kFewGated = 4096, kFewBlock = 2048;
 
 }  // namespace forge

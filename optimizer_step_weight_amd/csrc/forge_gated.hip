@@ -120,7 +120,7 @@ __global__ __launch_bounds__(THREADS, 1) void gated_kernel(GatedArgs a) {
 }  // namespace grp
 
 int launch_grouped_gated(const GatedArgs& given, void* stream) {
-  if (given.keep.type < FORGE_KEEP_FP8 && few_rows_call(given.T, given.E, given.N, 64)) return launch_gated_few(given, stream);
+  if (given.keep.type < FORGE_KEEP_FP8 && few_rows_call(given.T, given.E, given.N, 64, kFewGated)) return launch_gated_few(given, stream);
   GatedArgs a = given;
   const int64_t O = 2 * a.N;
   const int64_t row_tiles = a.T / 256 + (a.E < a.T ? a.E : a.T) + 1;
