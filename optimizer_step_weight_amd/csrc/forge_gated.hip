@@ -28,9 +28,28 @@ __device__ __forceinline__ void open_pair(Feed<S>& f, const void* first, uint32_
 // thread covers whole lines of a row (16 columns in one piece: gate and up in bf16 205 -> 212 us for 16384 rows of
 // 32 experts of 1408 x 2048), and the work on a block's scale is shared by half as many threads as 8 columns would
 // have (8192 x 14336 x 4096, codes: 1445 -> 1375 us).
+//
+// Addresses are the tile's, the same in all lanes, and 32-bit offsets in it (at most 256 rows of 2^20 columns).
+struct GatedOut {
+  unsigned char *h, *g, *u;   // of the tile's first row and column
+  float *gs, *us;             // its scales
+  uint32_t ld_h, ld_gu, ld_s; // bytes from row to row
+  __device__ __forceinline__ GatedOut(const GatedArgs& a, int64_t row0, int64_t n0) {
+    const int esz = a.keep.type == FORGE_KEEP_BF16 ? 2 : 1;
+    h = reinterpret_cast<unsigned char*>(a.H + row0 * a.N + n0);
+    g = static_cast<unsigned char*>(a.keep.data) + (row0 * 2 * a.N + n0) * esz;
+    u = g + a.N * esz;
+    gs = a.keep.scale + row0 * (a.N / 64) + n0 / 128;
+    us = gs + a.N / 128;
+    ld_h = (uint32_t)(2 * a.N);
+    ld_gu = (uint32_t)(2 * a.N * esz);
+    ld_s = (uint32_t)(a.N / 64);
+  }
+};
+
 template <int HALF>
-__device__ __forceinline__ void gated_row(const GatedArgs& a, int64_t row, int64_t n, bool live, const float (&g)[16],
-                                          const float (&u)[16]) {
+__device__ __forceinline__ void gated_row(const GatedArgs& a, const GatedOut& o, int row, int col, bool live,
+                                          const float (&g)[16], const float (&u)[16]) {
   float h[16];
   by_act(a.act, [&](auto act) {
 #pragma unroll
@@ -40,32 +59,32 @@ __device__ __forceinline__ void gated_row(const GatedArgs& a, int64_t row, int64
       h[i] = v * u[i];
     }
   });
-  auto put = [&](uint16_t* p, const float (&v)[16]) {
+  auto put = [&](unsigned char* base, uint32_t at, const float (&v)[16]) {
     if (!live) return;
-    st16_stream(p, to_bf16x8(v));
-    st16_stream(p + HALF, to_bf16x8(v + 8));
+    st16_stream(base + at, to_bf16x8(v));
+    st16_stream(base + at + 2 * HALF, to_bf16x8(v + 8));
   };
-  put(a.H + row * a.N + n, h);
+  put(o.h, (uint32_t)row * o.ld_h + 2u * (uint32_t)col, h);
   if (a.keep.type == FORGE_KEEP_BF16) {
-    uint16_t* p = static_cast<uint16_t*>(a.keep.data) + row * 2 * a.N + n;
-    put(p, g);
-    put(p + a.N, u);
+    const uint32_t at = (uint32_t)row * o.ld_gu + 2u * (uint32_t)col;
+    put(o.g, at, g);
+    put(o.u, at, u);
   }
   if constexpr (HALF == 64) {  // 8 lanes have a block's 128 columns
     auto eight = [&](auto qc) {
       constexpr int Q = decltype(qc)::value;
-      auto part = [&](const float (&v)[16], int64_t col) {
+      const uint32_t at = (uint32_t)row * o.ld_gu + (uint32_t)col;
+      auto part = [&](const float (&v)[16], unsigned char* base, float* scales) {
         const float scale = block_scale<Q>(max8(amax_bits(v)));
         if (!live) return;
         uint32_t q[4];
         encode<Q>(v, scale, q);
-        uint8_t* p = static_cast<uint8_t*>(a.keep.data) + row * 2 * a.N + col;
-        store_codes<false>(p, u32x2{q[0], q[1]}, 8);
-        store_codes<false>(p + HALF, u32x2{q[2], q[3]}, 8);
-        if ((threadIdx.x & 7) == 0) a.keep.scale[row * (a.N / 64) + (col >> 7)] = scale;
+        store_codes<false>(base + at, u32x2{q[0], q[1]}, 8);
+        store_codes<false>(base + at + HALF, u32x2{q[2], q[3]}, 8);
+        if ((threadIdx.x & 7) == 0) scales[(uint32_t)row * o.ld_s] = scale;
       };
-      part(g, n);
-      part(u, a.N + n);
+      part(g, o.g, o.gs);
+      part(u, o.u, o.us);
     };
     if (a.keep.type == FORGE_KEEP_FP8) eight(std::integral_constant<int, FORGE_Q_FP8>{});
     if (a.keep.type == FORGE_KEEP_I8) eight(std::integral_constant<int, FORGE_Q_I8>{});
@@ -87,6 +106,7 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& a, const RowTile& t,
   tile.contract(smem, fa, fb, slabs);
   using R = Rounds<HEIGHT, WIDTH>;
   constexpr int LANES = 2 * WIDTH;  // of a row
+  const GatedOut out(a, t.row0, n0);
   by_rounds<HEIGHT, WIDTH>(smem, tile, [&](int round) {
     const int p = (int)threadIdx.x % LANES;
     for (int r = (int)threadIdx.x / LANES; r < R::ROWS; r += THREADS / LANES) {
@@ -96,7 +116,7 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& a, const RowTile& t,
       R::get(smem, r, 2 * p + 4 * WIDTH, g + 8);
       R::get(smem, r, 2 * p + 8 * WIDTH, u);
       R::get(smem, r, 2 * p + 12 * WIDTH, u + 8);
-      gated_row<16 * WIDTH>(a, t.row0 + row, n0 + 8 * p, row < t.rows, g, u);
+      gated_row<16 * WIDTH>(a, out, row, 8 * p, row < t.rows, g, u);
     }
   });
 }

@@ -86,7 +86,18 @@ __device__ __forceinline__ void gated_dgrad_out(const GatedDgradArgs& a, const R
   constexpr int LANES = 8 * WIDTH, PER = THREADS / LANES;
   static_assert(K::ROWS % (2 * PER) == 0, "whole passes");
   const int p = (int)threadIdx.x % LANES, lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-  const int64_t n = n0 + 8 * p;
+  // Stores are range-checked: rows behind the tile's last are dropped, but every wave issues the same stores, as the
+  // waits below count them (loads and stores of a wave complete in order).
+  const uint32_t ld = (uint32_t)(2 * a.N);
+  const uint16_t* first = a.dGU + (int64_t)t.row0 * 2 * a.N + n0;
+  auto range = [](const uint16_t* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, (int)bytes, 0x00020000);
+  };
+  const auto rd = range(first, (uint32_t)t.rows * 2 * ld - (uint32_t)(2 * n0));
+  const auto rh = range(a.H ? a.H + (int64_t)t.row0 * a.N + n0 : nullptr, a.H ? (uint32_t)t.rows * ld - (uint32_t)(2 * n0) : 0u);
+  auto store = [](const u32x4& q, __amdgpu_buffer_rsrc_t rsrc, uint32_t at) {
+    __builtin_amdgcn_raw_buffer_store_b128(q, rsrc, at, 0, 2);  // 2: streaming
+  };
   const bool none = t.e == a.E;  // rows of no group
   auto chunk = [&](int r, int c) { return reinterpret_cast<floatx4*>(smem + r * 256 * WIDTH + 16 * (c ^ (r & 15))); };
   K kept;
@@ -104,11 +115,18 @@ __device__ __forceinline__ void gated_dgrad_out(const GatedDgradArgs& a, const R
         for (int j = 0; j < T::NB; ++j)
           *chunk((wave >> 1) * 16 + (lane & 15), (wave & 1) * 4 * T::NB + 4 * j + (lane >> 4)) = tile.acc[i][j];
     });
-    // this round's copies have landed: at most those of the next two are under way (the stores between them count
-    // too, so the wait is a little longer than it has to be)
-    if (round + 2 < K::N) wait_vm<2 * K::DMA>();
-    else if (round + 1 < K::N) wait_vm<K::DMA>();
-    else wait_vm<0>();
+    // this round's copies have landed; those of the next two rounds may be under way, and the last round's stores
+    constexpr int S = 3 * K::ROWS / PER;
+    if (round == 0) {
+      if (K::N > 2) wait_vm<2 * K::DMA>();
+      else wait_vm<K::DMA>();
+    } else if (round + 2 < K::N) {
+      wait_vm<2 * K::DMA + S>();
+    } else if (round + 1 < K::N) {
+      wait_vm<K::DMA + S>();
+    } else {
+      wait_vm<S>();
+    }
     __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4));  // LDS
     barrier();
     // two passes over the threads at a time, or their waits for LDS and the exponentials would be in the open
@@ -135,16 +153,13 @@ __device__ __forceinline__ void gated_dgrad_out(const GatedDgradArgs& a, const R
             g[i][j] = d[i][j] * u[i][j] * s;
             u[i][j] = d[i][j] * v;
           }
-          const int tr = K::tile_row(round, r + PER * i);
-          if (tr >= t.rows) continue;
+          const uint32_t at = (uint32_t)K::tile_row(round, r + PER * i) * ld, lane_at = 16u * (uint32_t)p;
           if (none)
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[i][j] = u[i][j] = h[i][j] = 0.0f;
-          const int64_t row = t.row0 + tr;
-          uint16_t* o = a.dGU + row * 2 * a.N + n;
-          st16_stream(o, to_bf16x8(g[i]));
-          st16_stream(o + a.N, to_bf16x8(u[i]));
-          if (a.H) st16_stream(a.H + row * a.N + n, to_bf16x8(h[i]));
+          store(to_bf16x8(g[i]), rd, 2 * at + lane_at);
+          store(to_bf16x8(u[i]), rd, 2 * at + lane_at + ld);
+          store(to_bf16x8(h[i]), rh, at + lane_at);
         }
       }
     });
