@@ -269,7 +269,8 @@ class FusedGatedExperts(torch.nn.Module):
 
     forward(x, ends): the rows of x [rows, width] are sorted by expert, ends[e] (int32, on the device) is the
     first row after expert e.  With one expert (a dense block) ends may be left out, and x have any leading
-    dimensions."""
+    dimensions.  Under torch.no_grad() nothing is kept, and the call may be captured into a graph; a training step
+    may not (its step count is the host's)."""
 
     def __init__(self, experts: int, width: int, hidden: int, *, act: str = "silu", opt: str = "adamw", hyper=None,
                  state_dtype: str = "f32", seed: int = 0, checkpoint: Optional[str] = None, device="cuda"):
@@ -295,7 +296,16 @@ class FusedGatedExperts(torch.nn.Module):
         elif x.dim() != 2 or ends.numel() != self.gate_up.experts:
             raise ValueError(f"with ends [{self.gate_up.experts}], x must be [rows, {self.width}] "
                              f"(got {ends.numel()} ends, {tuple(x.shape)})")
-        y = _GatedStep.apply(_packed(x.to(torch.bfloat16)), self.gate_up._anchor, ends, self)
+        x = _packed(x.to(torch.bfloat16))
+        if torch.is_grad_enabled():
+            if x.is_cuda and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("a captured training step would repeat its step count: capture the library's calls instead")
+            y = _GatedStep.apply(x, self.gate_up._anchor, ends, self)
+        else:
+            hidden = torch.empty(x.shape[0], self.hidden, dtype=torch.bfloat16, device=x.device)
+            y = torch.empty_like(x)
+            grouped_gated(x, self.gate_up.weight, ends, hidden, act=self.act)
+            grouped_gemm(hidden, self.down.weight, ends, y)
         return y.reshape(*lead, self.width)
 
     def extra_repr(self) -> str:

@@ -194,6 +194,8 @@ def A(monkeypatch):
         gu, _ = R.grouped(X, W, ends, True)
         n = H.shape[1]
         H.copy_(R.act(act, gu[:, :n])[0] * gu[:, n:])
+        if gate_up is None:
+            return
         if gate_up_scale is None:
             gate_up.copy_(gu)
         else:
@@ -244,6 +246,25 @@ def test_gated_layer_gradients(A, how):
     for (X, dY, W, _), w in zip(steps, (ws[1], ws[0])):
         dW = torch.stack([dY[a:b].double().t() @ X[a:b].double() for a, b in ((0, 4), (4, T))])
         assert near(dW, w.grad)
+
+
+def test_gated_layer_without_gradients(A, monkeypatch):
+    """Under no_grad the same output, nothing kept, no step; a captured training step is refused."""
+    A, steps = A
+    torch.manual_seed(2)
+    layer = A.FusedGatedExperts(1, 128, 128, act="gelu", device="cpu")
+    x = torch.randn(3, 5, 128).to(torch.bfloat16)
+    y = layer(x)
+    real, kept = A.grouped_gated, []
+    monkeypatch.setattr(A, "grouped_gated", lambda *a, **k: (kept.append(k.get("gate_up")), real(*a, **k)))
+    with torch.no_grad():
+        z = layer(x)
+    assert torch.equal(y, z) and z.grad_fn is None and not steps and layer.down.step_count == 0 and kept == [None]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    layer(x)                                      # a CPU tensor is on no stream
+    monkeypatch.setattr(A, "_packed", lambda t: type("OnGPU", (), {"is_cuda": True, "shape": t.shape})())
+    with pytest.raises(RuntimeError, match="step count"):
+        layer(x)
 
 
 def test_gated_layer_arguments(A):

@@ -189,6 +189,25 @@ def calls(lib):
     return run, x, [H, gu, s, h1, d, H2, d2, q, sc, back, wq, ws, wt, wts, Y, Y1, dx, dg]
 
 
+def test_gated_layer_serves_from_a_graph(lib):
+    """One token under no_grad, captured and replayed with other tokens."""
+    from optimizer_step_weight_amd.autograd import FusedGatedExperts
+    layer = FusedGatedExperts(1, 256, 384, seed=1)
+    x = normal((1, 256), 1)
+    with torch.no_grad():
+        layer(x)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = layer(x)
+        for i in range(3):
+            x.copy_(normal((1, 256), 5 + i))
+            g.replay()
+            want = layer(x)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+
+
 def bits(t):
     return t.contiguous().view(torch.uint8).clone()
 
