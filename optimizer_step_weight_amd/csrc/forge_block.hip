@@ -2,7 +2,11 @@
 // (128 x 128) with a transposed copy, and the activation's backward pass that reads such codes.
 //
 // All are bound by memory: every element is read and written once.  A thread takes 8 consecutive columns,
-// 16 threads a block, whose largest magnitude they find by rotations among themselves.
+// 16 threads a block, whose largest magnitude they find by exchanges within the vector unit.
+//
+// 16384 x 5120 bf16 to int8 49 us and back 46 (5.3-5.5 TB/s); activation's backward pass of 4099 x 17408 from e4m3 112-116
+// us (6.2-6.4 TB/s); weights of 8 x 14336 x 4096 with the transposed copy 403 us (4.7 TB/s, a copy's rate; its bytes
+// turn in LDS, which is busy throughout but not what it waits for).
 #include <hip/hip_runtime.h>
 
 #include "forge_act.h"

@@ -4,14 +4,21 @@
 // A block's sum is multiplied by its scales before the next is added, so the matrix cores cannot keep the
 // whole contraction in their accumulators: each 16 x 16 block of the output takes one 16 x 16 x 128 product
 // from zero (32 cycles) and 4 multiply-adds on the vector unit (16 cycles), which run beside the next
-// block's products.  The vector unit cannot read the accumulation registers, so a wave keeps 128 x 64 of
-// the output in 128 vector registers, and 8 waves (two a SIMD) a tile of 256 x 256.  (32 x 32 x 64 products,
-// two from zero for each block, need 32 registers instead of 16 for results that wait.)
+// block's products.  The vector unit cannot read the accumulation registers, so a wave keeps 112 x 64 of
+// the output in 112 vector registers, and 8 waves (two a SIMD) a tile of 224 x 256.  (32 x 32 x 64 products,
+// two from zero for each block, need 64 registers instead of 16 for results that wait.)
 //
-// A slab is one block of the contraction, 128 bytes of a row, copied to LDS by DMA in whole lines; LDS holds
-// two.  The scales of 8 slabs are loaded 8 slabs ahead and pass through LDS, by slab and row.
+// A slab is one block of the contraction, 128 bytes of a row, copied to LDS by DMA in whole lines.  LDS holds three
+// slabs of X and two of W, whose fragments a wave reads half a slab ahead: with one barrier a slab, all of
+// a slab's copies have most of a slab's time to land, and they go out at an even pace.  224 rows a tile leave room for
+// the scales: those of 4 slabs are copied 4 slabs ahead, by row, where they lie on 16 bytes, else by slab.
 //
-// 16384 rows of 8 uneven experts by 14336 x 4096: 1038 us, 1.85 PFLOP/s.
+// 16384 rows of 8 uneven experts by 14336 x 4096: 979-1032 us over the cards seen, 1.86-1.97 PFLOP/s (row scales,
+// forge_grouped.h: 845-860); in even groups 832-847 us, 2.25 PFLOP/s.  A longer contraction adds 2.4 PFLOP/s.  What bounds
+// it is LDS: fragments and copies together move 240 KiB a slab, 1900 cycles at 128 bytes each beside the
+// products' 1792.  Without the copies' data the same loop takes 645 us, without those of X 765, with all of them
+// hits in L2 790.  4 waves of 96 x 128 read less from LDS, but a wave alone on its SIMD then issues everything: 872 us.
+// Copies in bursts 888 us; one slab of each ahead and W's fragments read when they are used 930.
 #include <hip/hip_runtime.h>
 
 #include "forge_ffn_internal.h"
