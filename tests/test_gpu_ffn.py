@@ -355,6 +355,83 @@ def test_block_product(lib, T, E, N, K):
     assert torch.equal(Y, again)
 
 
+@pytest.mark.parametrize("K", [128 * 63, 128 * 64, 128 * 65, 128 * 66, 128 * 132])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_block_product_long_contractions(lib, K, shift):
+    """More blocks than their weights' scales are held for at once; scales of X on 16 bytes and beside them."""
+    T, E, N = 300, 2, 384
+    X, W = codes((T, K), T), codes((E, N, K), N)
+    g = gen(3)
+    xs, ws = 0.1 + torch.rand(T, K // 128, generator=g), 0.003 * (0.1 + torch.rand(E, N // 128, K // 128, generator=g))
+    ends = torch.tensor([190, 300], dtype=torch.int32)
+    buf = torch.empty(xs.numel() + 4, device="cuda")
+    xd = buf[shift:shift + xs.numel()].view(xs.shape)
+    xd.copy_(xs)
+    Y = torch.full((T, N), float("nan"), dtype=BF, device="cuda")
+    lib.grouped_block_gemm(X.cuda(), xd, W.cuda(), ws.cuda(), ends.cuda(), Y)
+    want, off = block_reference(X, xs, W, ws, ends)
+    near(Y, want, off + HALF[BF] * (want.abs() + off) + 2.0 ** -133)
+
+
+def test_products_past_32_bits(lib):
+    """Outputs of more than 2^31 elements; rows at both ends and beside the groups' border."""
+    T, N, K, ends = 150_000, 8192, 128, [75_001, 150_000]
+    X, W, Wd = normal((T, K), 1), normal((2, 2 * N, K), 2, K ** -0.5), normal((2, K, N), 3, K ** -0.5)
+    rows = torch.cat([torch.arange(a, b) for a, b in ((0, 40), (74_980, 75_020), (T - 40, T))])
+    at = (rows >= ends[0]).long()
+    Xd, Wc, ed = X.cuda(), W.cuda(), torch.tensor(ends, dtype=torch.int32, device="cuda")
+    H, gu = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, 2 * N, dtype=BF, device="cuda")
+    x, w = X[rows].to(R.F64), W.to(R.F64)
+    want = torch.stack([x[i] @ w[at[i]].t() for i in range(len(rows))])
+    off = K * R.U * torch.stack([x[i].abs() @ w[at[i]].abs().t() for i in range(len(rows))])
+    lib.grouped_gated(Xd, Wc, ed, H, gate_up=gu, act="relu")
+    near(gu[rows], want, off + HALF[BF] * (want.abs() + off) + 2.0 ** -133)
+    h = want[:, :N].clamp(min=0) * want[:, N:]
+    oh = off[:, :N] * (want[:, N:].abs() + off[:, N:]) + want[:, :N].abs() * off[:, N:] + 2 * R.U * h.abs()
+    near(H[rows], h, oh + HALF[BF] * (h.abs() + oh) + 2.0 ** -133)
+    for kind in (FP8, I8):
+        q, s = torch.empty(T, 2 * N, dtype=kind, device="cuda"), torch.empty(T, 2 * N // 128, device="cuda")
+        lib.grouped_gated(Xd, Wc, ed, H, gate_up=q, gate_up_scale=s, act="relu")
+        top = s[rows].cpu().to(R.F64).repeat_interleave(128, 1)
+        step = HALF[FP8] * want.abs() + 2.0 ** -10 * top if kind is FP8 else 0.5 * top
+        near(R.value(q[rows].cpu(), s[rows].cpu()), want, (1 + 8 * R.U * R.MOST[kind]) * step + 1.1 * off)
+    # the backward pass from the int8 codes
+    d = gu
+    lib.grouped_gated_dgrad(Xd, Wd.cuda(), ed, q, d, H=H, gate_up_scale=s, act="relu")
+    v = R.value(q[rows].cpu(), s[rows].cpu())
+    wd = Wd.to(R.F64)
+    dh = torch.stack([x[i] @ wd[at[i]] for i in range(len(rows))])
+    odh = K * R.U * torch.stack([x[i].abs() @ wd[at[i]].abs() for i in range(len(rows))])
+    on = (v[:, :N] > 0).to(R.F64)
+    for got, f in ((d[rows][:, :N], v[:, N:] * on), (d[rows][:, N:], v[:, :N] * on)):
+        o = (odh + 8 * R.U * dh.abs()) * f.abs()
+        near(got, dh * f, o + HALF[BF] * ((dh * f).abs() + o) + 2.0 ** -133)
+    d2 = torch.empty_like(d)
+    lib.gated_backward(H, q, d2, gate_up_scale=s, act="relu")
+    hr = H[rows].cpu().to(R.F64)
+    near(d2[rows][:, N:], hr * v[:, :N] * on, (HALF[BF] + 8 * R.U) * (hr * v[:, :N]).abs() + 2.0 ** -133)
+
+
+def test_ends_out_of_order_are_clamped(lib):
+    """As the grouped products take them."""
+    ends, T, N, K = [-5, 60, 40, 10 ** 6, 100], 130, 128, 256
+    ed = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    fine = torch.tensor([0, 60, 60, 130, 130], dtype=torch.int32, device="cuda")
+    X, W, Wd = normal((T, K), 1).cuda(), normal((5, 2 * N, K), 2).cuda(), normal((5, K, N), 3).cuda()
+    q, s = R.quantize(X.cpu(), FP8)
+    wq, ws = R.quantize_weight(W.cpu())
+    gu = normal((T, 2 * N), 4).cuda()
+    for rows in (T, 5):
+        got = []
+        for e in (ed, fine):
+            H, d, Y = (torch.full((rows, n), 7.0, dtype=BF, device="cuda") for n in (N, 2 * N, 2 * N))
+            lib.grouped_gated(X[:rows], W, e, H)
+            lib.grouped_gated_dgrad(X[:rows], Wd, e, gu[:rows], d)
+            lib.grouped_block_gemm(q.cuda()[:rows], s.cuda()[:rows], wq.cuda(), ws.cuda(), e, Y)
+            got.append((H, d, Y))
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_block_product_exact_and_bad_blocks(lib):
     """Small whole numbers and scales that are powers of two: exact.  A NaN scale or code spoils its row, or its
     columns of its group, alone."""
