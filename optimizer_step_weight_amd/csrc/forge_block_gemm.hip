@@ -83,7 +83,7 @@ __device__ __forceinline__ void block_tile(const BlockGemmArgs& a, const RowTile
       for (int i = 0; i < 2; ++i) {
         const int g = 2 * wave + i, s = 4 * c + (g >> 2), r = 64 * (g & 3) + lane;
         const uint32_t o = s < KB ? (uint32_t)(r * KB + s) * 4u : 0xFFFFFFF0u;
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at + (uint32_t)(g * 256)), "v"(o), "s"(rs)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(at + (uint32_t)(g * 256)), "v"(o), "s"(rs)
                      : "memory", "m0");
       }
     }

@@ -71,7 +71,7 @@ struct KeptRounds {
   static __device__ __forceinline__ void copy_256(const u32x4& rs, uint32_t o, uint32_t to) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(o), "s"(rs) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(o), "s"(rs) : "memory", "m0");
 #pragma clang diagnostic pop
   }
   // Columns 8 p .. of row r of gate (part 0) or up.

@@ -209,14 +209,15 @@ struct Side {
   static __device__ __forceinline__ int swz(int r) { return TR ? 4 * (r & 3) + 2 * ((r / R_LANE) & 1) : (r >> 1) & 7; }
 };
 
-// One copy of 1 KiB: 16 bytes a lane from rsrc + off to LDS address `lds` + AT + 16 lane.  Two
-// instructions, because a wave issues one in 4 cycles: three fit beside a 16 x 16 x 32 product, and
-// more would keep the matrix core waiting.  Completion is awaited with wait_vm.
+// One copy of 1 KiB: 16 bytes a lane from rsrc + off to LDS address `lds` + AT + 16 lane.  Three
+// instructions, with the wait state between M0 and the copy that reads it: a wave issues one in 4 cycles, so
+// three fit beside a 16 x 16 x 32 product, and more would keep the matrix core waiting.  Completion is awaited
+// with wait_vm.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 template <int AT>
 __device__ __forceinline__ void copy_1k(const u32x4& rsrc, uint32_t off, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(lds), "i"(AT), "v"(off), "s"(rsrc)
+  asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(lds), "i"(AT), "v"(off), "s"(rsrc)
                : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop

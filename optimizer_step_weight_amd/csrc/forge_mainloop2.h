@@ -87,12 +87,14 @@ __device__ __forceinline__ u32x4 make_rsrc(const void* base, uint32_t bytes) {
 // One 16-byte-per-lane copy global -> LDS (lane l lands at lds + 16 l).  Issued as inline asm
 // so that the compiler does not add a wait for it before every LDS read (it cannot prove the
 // copy and the reads touch different stages); completion is awaited explicitly with wait_vm.
+// Copies to LDS read M0 one wait state after a scalar instruction has written it at the earliest; within
+// one asm the compiler does not add it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const u32x4& rsrc, uint32_t voff, const unsigned char* lds) {
   const uint32_t la =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(la), "v"(voff), "s"(rsrc)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(la), "v"(voff), "s"(rsrc)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
