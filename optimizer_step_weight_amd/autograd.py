@@ -319,22 +319,24 @@ class _RMSNorm(torch.autograd.Function):
         y = torch.empty_like(x)
         rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
         rmsnorm(x, gain, y, residual=residual, h=h, rstd=rstd, eps=eps)
-        ctx.save_for_backward(gain, rstd, *_keep(x if h is None else h, codes))
+        # with codes an empty output: saved, it connects the gradients to x and residual, as h does where it is kept whole
+        tie = None if codes is None else torch.empty(0, device=x.device)
+        ctx.save_for_backward(gain, rstd, tie, *_keep(x if h is None else h, codes))
         ctx.alone = h is None
         ctx.set_materialize_grads(False)
-        return y if h is None else (y, h)
+        return (y, tie) if h is None else (y, tie, h)
 
     @staticmethod
-    def backward(ctx, dy, dh=None):
-        gain, rstd, *h = ctx.saved_tensors
+    def backward(ctx, dy, _, dh=None):
+        gain, rstd, tie, *h = ctx.saved_tensors
         if dy is None:   # only the stream was used
             return dh, dh, None, None, None
         grads = _RMSNormGrad.apply if torch.is_grad_enabled() else _norm_grads
-        dx, dgain = grads(dy, dh, gain, rstd, ctx.needs_input_grad[2], *h)
+        dx, dgain = grads(dy, dh, gain, rstd, tie, ctx.needs_input_grad[2], *h)
         return dx, None if ctx.alone else dx, dgain, None, None
 
 
-def _norm_grads(dy, dh, gain, rstd, want_gain, h, scale=None):
+def _norm_grads(dy, dh, gain, rstd, tie, want_gain, h, scale=None):
     dx = torch.empty(h.shape, dtype=dy.dtype, device=h.device)
     dgain = torch.empty(gain.shape, dtype=torch.float32, device=h.device) if want_gain else None
     rmsnorm_backward(_packed(dy), h, gain, rstd, dx, dgain, dh=None if dh is None else _packed(dh),
@@ -373,9 +375,9 @@ class RMSNorm(torch.nn.Module):
         if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
             raise ValueError("residual must have the shape and dtype of x")
         flat = lambda t: _packed(t.reshape(-1, self.width))  # noqa: E731
-        out = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), _packed(self.gain), self.eps,
-                             self.codes)
-        return out.view(x.shape) if residual is None else tuple(t.view(x.shape) for t in out)
+        y, _, *h = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), _packed(self.gain), self.eps,
+                                  self.codes)
+        return y.view(x.shape) if residual is None else (y.view(x.shape), h[0].view(x.shape))
 
     def extra_repr(self) -> str:
         return f"width={self.width}, eps={self.eps}"

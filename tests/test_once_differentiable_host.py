@@ -1,0 +1,80 @@
+"""Second derivatives of the autograd layers on the CPU, with stand-ins for the library's calls: what the library computes
+has no graph, so a gradient that depends on what it is differentiated by raises, in every way that it can be kept."""
+import pytest
+import torch
+
+from tests import ffn_ref as R
+from tests import layer_ref as L
+
+
+@pytest.fixture()
+def A(monkeypatch):
+    from optimizer_step_weight_amd import autograd
+
+    def rmsnorm(x, gain, y, *, residual=None, h=None, rstd=None, eps):
+        s = x.detach() if residual is None else (x.detach().float() + residual.detach().float()).to(x.dtype)
+        out, r = L.norm(s.double(), gain.detach().double(), eps)
+        y.data.copy_(out), rstd.data.copy_(r)
+        if h is not None:
+            h.data.copy_(s)
+
+    def rmsnorm_backward(dy, h, gain, rstd, dx, dgain=None, *, dh=None, h_scale=None):
+        h = h.detach().double() if h_scale is None else R.value(h, h_scale)
+        gx, gg = L.norm_grads(dy.detach().double(), h, gain.detach().double(), rstd.detach().double(),
+                              None if dh is None else dh.detach().double())
+        dx.data.copy_(gx)
+        if dgain is not None:
+            dgain.data.copy_(gg)
+    monkeypatch.setattr(autograd, "rmsnorm", rmsnorm)
+    monkeypatch.setattr(autograd, "rmsnorm_backward", rmsnorm_backward)
+    monkeypatch.setattr(autograd, "block_quantize",
+                        lambda x, q, s: [a.copy_(b) for a, b in zip((q, s), R.quantize(x.detach(), q.dtype))])
+    return autograd
+
+
+HOW = [None, "int8", "fp8"]
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("frozen", [False, True])
+@pytest.mark.parametrize("linear", [False, True])
+@pytest.mark.parametrize("how", HOW)
+def test_norm(A, how, linear, frozen, residual):
+    """Also where only the kept input ties the gradient to x: a constant gradient arrives, and the gain is frozen."""
+    torch.manual_seed(1)
+    norm = A.RMSNorm(200, checkpoint=how, device="cpu")
+    norm.gain.requires_grad_(not frozen)
+    x, up = torch.randn(3, 200, requires_grad=True), torch.randn(3, 200)
+
+    def gradient(create_graph, z):
+        y = norm(z, z + 1)[0] if residual else norm(z)
+        return torch.autograd.grad((y * up if linear else y.square()).sum(), x, create_graph=create_graph)[0]
+    for z in (lambda: x, x.square):            # x itself, and what can be differentiated twice
+        first = gradient(True, z())
+        assert first.requires_grad
+        with pytest.raises(RuntimeError, match="once only"):
+            torch.autograd.grad(first.square().sum() + x.square().sum(), x)
+        assert torch.equal(first, gradient(False, z()))      # once is as it is without a graph
+
+
+@pytest.mark.parametrize("how", HOW)
+def test_norm_gain(A, how):
+    """The gain's gradient depends on x too."""
+    norm = A.RMSNorm(200, checkpoint=how, device="cpu")
+    x = torch.randn(3, 200, requires_grad=True)
+    dgain, = torch.autograd.grad(norm(x).sum(), norm.gain, create_graph=True)
+    with pytest.raises(RuntimeError, match="once only"):
+        torch.autograd.grad(dgain.square().sum() + x.sum(), x)
+
+
+@pytest.mark.parametrize("how", ["int8", "fp8"])
+def test_norm_keeps_codes_alone(A, how):
+    """What refuses a second derivative holds no memory: between the passes there are the codes, scales and row scales."""
+    norm = A.RMSNorm(256, checkpoint=how, device="cpu")
+    x = torch.randn(8, 256, requires_grad=True)
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t.untyped_storage().nbytes()) or t, lambda t: t):
+        y = norm(x)
+    assert sorted(kept, reverse=True)[:2] == [8 * 256, 4 * 256] and sum(kept) == 8 * 256 + 4 * 256 + 4 * 8 * 2 + 4 * 8
+    y.sum().backward()
+    assert x.grad is not None and norm.gain.grad is not None
