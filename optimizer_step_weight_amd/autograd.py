@@ -69,6 +69,23 @@ def _kept(saved) -> torch.Tensor:
     return x2d
 
 
+class _Once(torch.autograd.Function):
+    """The tensor in `out`, computed by the library, connected to the tensors that it depends on under create_graph, so
+    that differentiating it again is refused instead of passing the layer over."""
+
+    @staticmethod
+    def forward(ctx, out, *sources):
+        return out[0]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this layer can be differentiated once only: its gradients have no gradient")
+
+
+def _once(dx, *sources):
+    return dx if dx is None or not torch.is_grad_enabled() else _Once.apply([dx], *sources)
+
+
 class _LinearStep(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x2d, anchor, layer):
@@ -237,13 +254,15 @@ class _GatedStep(torch.autograd.Function):
             scale = new(2 * layer.hidden // 128, torch.float32)
         grouped_gated(x2d, up.weight, ends, hidden, gate_up=kept, gate_up_scale=scale, act=layer.act)
         grouped_gemm(hidden, down.weight, ends, y)   # `hidden` is not kept: the backward pass has it from gate and up
-        ctx.save_for_backward(ends, kept, scale, *_keep(x2d, up.codes))
-        return y
+        # with codes an empty output: saved, it connects the gradient to x, as x itself does
+        tie = None if up.codes is None else new(0)
+        ctx.save_for_backward(ends, kept, scale, tie, *_keep(x2d, up.codes))
+        return y, tie
 
     @staticmethod
-    def backward(ctx, dy):
-        ends, kept, scale, *saved = ctx.saved_tensors
-        layer = ctx.layer
+    def backward(ctx, dy, _):
+        ends, kept, scale, tie, *saved = ctx.saved_tensors
+        layer, arriving = ctx.layer, dy
         up, down = layer.gate_up, layer.down
         dy = _packed(dy.to(torch.bfloat16))
         grad = torch.empty(kept.shape, dtype=torch.bfloat16, device=kept.device)
@@ -256,7 +275,7 @@ class _GatedStep(torch.autograd.Function):
             dx = torch.empty(kept.shape[0], up.in_features, dtype=torch.bfloat16, device=kept.device)
             grouped_dgrad(grad, up.weight, ends, dx)
         _step_experts(up, _kept(saved), grad, ends)
-        return dx, None, None, None
+        return _once(dx, arriving, tie, saved[0]), None, None, None
 
 
 class FusedGatedExperts(torch.nn.Module):
@@ -265,7 +284,8 @@ class FusedGatedExperts(torch.nn.Module):
     rows, then up rows) and of `down` [experts, width, hidden], both FusedExperts.  width and hidden are
     multiples of 128.  act: silu, gelu, gelu_tanh or relu.  checkpoint: None, "int8" or "fp8": how gate,
     up and the input are kept; the product of gate and up is not kept at all.  The other arguments, the limits
-    and one backward for each forward are FusedLinear's; seed goes to gate_up and seed + 1 to down.
+    and one backward for each forward are FusedLinear's; seed goes to gate_up and seed + 1 to down.  It can be differentiated
+    once: a second derivative raises.
 
     forward(x, ends): the rows of x [rows, width] are sorted by expert, ends[e] (int32, on the device) is the
     first row after expert e.  With one expert (a dense block) ends may be left out, and x have any leading
@@ -300,7 +320,7 @@ class FusedGatedExperts(torch.nn.Module):
         if torch.is_grad_enabled():
             if x.is_cuda and torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a captured training step would repeat its step count: capture the library's calls instead")
-            y = _GatedStep.apply(x, self.gate_up._anchor, ends, self)
+            y, _ = _GatedStep.apply(x, self.gate_up._anchor, ends, self)
         else:
             hidden = torch.empty(x.shape[0], self.hidden, dtype=torch.bfloat16, device=x.device)
             y = torch.empty_like(x)

@@ -78,3 +78,56 @@ def test_norm_keeps_codes_alone(A, how):
     assert sorted(kept, reverse=True)[:2] == [8 * 256, 4 * 256] and sum(kept) == 8 * 256 + 4 * 256 + 4 * 8 * 2 + 4 * 8
     y.sum().backward()
     assert x.grad is not None and norm.gain.grad is not None
+
+
+@pytest.fixture()
+def layers(A, monkeypatch):
+    def product(x, w, ends, out, nt):
+        out.data.copy_(R.grouped(x.detach(), w, ends, nt)[0])
+
+    def grouped_gated(X, W, ends, H, *, gate_up=None, gate_up_scale=None, act):
+        gu, n = R.grouped(X.detach(), W, ends, True)[0], H.shape[1]
+        H.copy_(R.act(act, gu[:, :n])[0] * gu[:, n:])
+        if gate_up_scale is not None:
+            q, s = R.quantize(gu, gate_up.dtype)
+            gate_up.copy_(q), gate_up_scale.copy_(s.view(gate_up_scale.shape))
+        elif gate_up is not None:
+            gate_up.copy_(gu)
+
+    def grouped_gated_dgrad(dY, W, ends, gate_up, dgate_up, *, H=None, gate_up_scale=None, act):
+        v, n = gate_up.double() if gate_up_scale is None else R.value(gate_up, gate_up_scale), H.shape[1]
+        (dg, du, h), _ = R.gated_grads(act, R.grouped(dY.detach(), W, ends, False)[0], v[:, :n], v[:, n:])
+        dgate_up.copy_(torch.cat([dg, du], 1)), H.copy_(h)
+    steps = []
+    monkeypatch.setattr(A, "grouped_gated", grouped_gated)
+    monkeypatch.setattr(A, "grouped_gated_dgrad", grouped_gated_dgrad)
+    monkeypatch.setattr(A, "grouped_gemm", lambda x, w, ends, y: product(x, w, ends, y, True))
+    monkeypatch.setattr(A, "grouped_dgrad", lambda x, w, ends, y: product(x, w, ends, y, False))
+    monkeypatch.setattr(A, "grouped_wgrad_step", lambda *a, **k: steps.append(k["step"]))
+    monkeypatch.setattr(A, "block_dequantize", lambda q, s, y: y.copy_(R.value(q, s)))
+    return A, steps
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("linear", [False, True])
+def test_gated(layers, how, linear):
+    """Its gradient depends on x through the activation, whatever arrives."""
+    A, steps = layers
+    torch.manual_seed(2)
+    block = A.FusedGatedExperts(2, 128, 128, checkpoint=how, device="cpu")
+    x, ends = torch.randn(5, 128, requires_grad=True), torch.tensor([2, 5], dtype=torch.int32)
+
+    def gradient(create_graph, z):
+        y = block(z, ends).float()
+        return torch.autograd.grad((y if linear else y.square()).sum(), x, create_graph=create_graph)[0]
+    for z in (lambda: x, x.square):
+        first = gradient(True, z())
+        assert first.requires_grad
+        with pytest.raises(RuntimeError, match="once only"):
+            torch.autograd.grad(first.square().sum() + x.square().sum(), x)
+        assert torch.equal(first, gradient(False, z()))
+    assert steps == [1, 1, 2, 2, 3, 3, 4, 4]
+    # a gradient that is kept with its graph can be cleared as any other
+    block(x, ends).sum().backward(create_graph=True)
+    torch.optim.SGD([x], lr=1.0).zero_grad(set_to_none=False)
+    assert not x.grad.any()
