@@ -96,7 +96,7 @@ class _LinearStep(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x2d = _kept(ctx.saved_tensors)
-        layer = ctx.layer
+        layer, arriving = ctx.layer, dy
         dy = _packed(dy.to(layer.weight.dtype))
         layer.step_count += 1
         kw = dict(opt=layer.opt, hyper=layer.hyper, step=layer.step_count, seed=layer.seed,
@@ -107,7 +107,7 @@ class _LinearStep(torch.autograd.Function):
         else:
             dx = None
             wgrad_step(x2d, dy, layer.weight, layer.m, layer.v, **kw)
-        return dx, None, None
+        return _once(dx, arriving), None, None
 
 
 class FusedLinear(torch.nn.Module):
@@ -120,6 +120,9 @@ class FusedLinear(torch.nn.Module):
     state_dtype: "f32" or "int8" (block-64 absmax moments).
     seed: the stochastic-rounding key of this layer (give every layer its own).
     checkpoint: None, "int8" or "fp8": how the input is kept for the backward pass.
+
+    The input's gradient dY W can be differentiated once: where the arriving gradient dY depends on what it is
+    differentiated by, a second derivative raises.
     """
 
     def __init__(self, in_features: int, out_features: int, *, opt: str = "adamw",
@@ -188,14 +191,14 @@ class _ExpertsStep(torch.autograd.Function):
     def backward(ctx, dy):
         ends, *saved = ctx.saved_tensors
         x2d = _kept(saved)
-        layer = ctx.layer
+        layer, arriving = ctx.layer, dy
         dy = _packed(dy.to(torch.bfloat16))
         dx = None
         if ctx.needs_input_grad[0]:   # with the weights as they were
             dx = torch.empty_like(x2d)
             grouped_dgrad(dy, layer.weight, ends, dx)
         _step_experts(layer, x2d, dy, ends)
-        return dx, None, None, None
+        return _once(dx, arriving), None, None, None
 
 
 def _step_experts(layer, x2d, dy, ends) -> None:

@@ -131,3 +131,30 @@ def test_gated(layers, how, linear):
     block(x, ends).sum().backward(create_graph=True)
     torch.optim.SGD([x], lr=1.0).zero_grad(set_to_none=False)
     assert not x.grad.any()
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("experts", [False, True])
+def test_linear_layers(layers, monkeypatch, experts, how):
+    """Their gradient depends on x through the arriving gradient alone: where that is constant, so is it."""
+    A, steps = layers
+
+    def linear_backward_step(x, dy, W, dx, m, v, **k):
+        dx.copy_(dy.detach() @ W)
+        steps.append(k["step"])
+    monkeypatch.setattr(A, "linear_backward_step", linear_backward_step)
+    torch.manual_seed(3)
+    layer = (A.FusedExperts(2, 128, 256, checkpoint=how, device="cpu") if experts
+             else A.FusedLinear(128, 256, checkpoint=how, device="cpu"))
+    x, args = torch.randn(5, 128, requires_grad=True), (torch.tensor([2, 5], dtype=torch.int32),) if experts else ()
+
+    def gradient(create_graph, linear):
+        y = layer(x, *args).float()
+        return torch.autograd.grad((y if linear else y.square()).sum(), x, create_graph=create_graph)[0]
+    first = gradient(True, False)
+    with pytest.raises(RuntimeError, match="once only"):
+        torch.autograd.grad(first.square().sum() + x.square().sum(), x)
+    assert torch.equal(first, gradient(False, False))
+    first = gradient(True, True)
+    assert torch.equal(torch.autograd.grad((first * x).sum(), x)[0], first)     # a constant gradient's penalty
+    assert steps == [1, 2, 3]
