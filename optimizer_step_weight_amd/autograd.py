@@ -281,6 +281,18 @@ class _GatedStep(torch.autograd.Function):
         return _once(dx, arriving, tie, saved[0]), None, None, None
 
 
+class _GatedServe(torch.autograd.Function):
+    """The output alone.  A function of autograd's because no_grad leaves forward-mode differentiation on, which it refuses."""
+
+    @staticmethod
+    def forward(ctx, x2d, ends, layer):
+        hidden = torch.empty(x2d.shape[0], layer.hidden, dtype=torch.bfloat16, device=x2d.device)
+        y = torch.empty_like(x2d)
+        grouped_gated(x2d, layer.gate_up.weight, ends, hidden, act=layer.act)
+        grouped_gemm(hidden, layer.down.weight, ends, y)
+        return y
+
+
 class FusedGatedExperts(torch.nn.Module):
     """y[t] = (act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)) Wd[e]^T for the rows t of expert e: a gated feed-forward
     block whose backward pass updates its weights, those of `gate_up` [experts, 2 hidden, width] (gate
@@ -325,10 +337,7 @@ class FusedGatedExperts(torch.nn.Module):
                 raise RuntimeError("a captured training step would repeat its step count: capture the library's calls instead")
             y, _ = _GatedStep.apply(x, self.gate_up._anchor, ends, self)
         else:
-            hidden = torch.empty(x.shape[0], self.hidden, dtype=torch.bfloat16, device=x.device)
-            y = torch.empty_like(x)
-            grouped_gated(x, self.gate_up.weight, ends, hidden, act=self.act)
-            grouped_gemm(hidden, self.down.weight, ends, y)
+            y = _GatedServe.apply(x, ends, self)
         return y.reshape(*lead, self.width)
 
     def extra_repr(self) -> str:
