@@ -50,6 +50,12 @@ def _checkpoint(how):
     return None if how is None else _CODES[how]
 
 
+def _codes_now(layer):
+    """The type of a layer's codes in this call: without gradients nothing is kept.  (Asked in the module: within a
+    function of autograd's gradients are off.)"""
+    return layer.codes if torch.is_grad_enabled() else None
+
+
 def _keep(x2d: torch.Tensor, codes):
     """x2d as it is kept for the backward pass: itself, or its codes and their scales."""
     if codes is None:
@@ -88,9 +94,9 @@ def _once(dx, *sources):
 
 class _LinearStep(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x2d, anchor, layer):
+    def forward(ctx, x2d, anchor, layer, codes):
         ctx.layer = layer
-        ctx.save_for_backward(*_keep(x2d, layer.codes))
+        ctx.save_for_backward(*_keep(x2d, codes))
         return x2d @ layer.weight.t()
 
     @staticmethod
@@ -107,7 +113,7 @@ class _LinearStep(torch.autograd.Function):
         else:
             dx = None
             wgrad_step(x2d, dy, layer.weight, layer.m, layer.v, **kw)
-        return _once(dx, arriving), None, None
+        return _once(dx, arriving), None, None, None
 
 
 class FusedLinear(torch.nn.Module):
@@ -171,7 +177,7 @@ class FusedLinear(torch.nn.Module):
             raise ValueError(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         lead = x.shape[:-1]
         x2d = _packed(x.reshape(-1, self.in_features).to(torch.bfloat16))
-        y = _LinearStep.apply(x2d, self._anchor, self)
+        y = _LinearStep.apply(x2d, self._anchor, self, _codes_now(self))
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self) -> str:
@@ -180,9 +186,9 @@ class FusedLinear(torch.nn.Module):
 
 class _ExpertsStep(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x2d, anchor, ends, layer):
+    def forward(ctx, x2d, anchor, ends, layer, codes):
         ctx.layer = layer
-        ctx.save_for_backward(ends, *_keep(x2d, layer.codes))
+        ctx.save_for_backward(ends, *_keep(x2d, codes))
         y = torch.empty(x2d.shape[0], layer.out_features, dtype=torch.bfloat16, device=x2d.device)
         grouped_gemm(x2d, layer.weight, ends, y)
         return y
@@ -198,7 +204,7 @@ class _ExpertsStep(torch.autograd.Function):
             dx = torch.empty_like(x2d)
             grouped_dgrad(dy, layer.weight, ends, dx)
         _step_experts(layer, x2d, dy, ends)
-        return _once(dx, arriving), None, None, None
+        return _once(dx, arriving), None, None, None, None
 
 
 def _step_experts(layer, x2d, dy, ends) -> None:
@@ -239,7 +245,7 @@ class FusedExperts(FusedLinear):
             raise ValueError(f"x must be [rows, {self.in_features}] (got {tuple(x.shape)})")
         if ends.numel() != self.experts:
             raise ValueError(f"ends must have {self.experts} entries (got {ends.numel()})")
-        return _ExpertsStep.apply(_packed(x.to(torch.bfloat16)), self._anchor, ends, self)
+        return _ExpertsStep.apply(_packed(x.to(torch.bfloat16)), self._anchor, ends, self, _codes_now(self))
 
     def extra_repr(self) -> str:
         return f"experts={self.experts}, " + super().extra_repr()
@@ -351,6 +357,8 @@ class _RMSNorm(torch.autograd.Function):
         y = torch.empty_like(x)
         rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
         rmsnorm(x, gain, y, residual=residual, h=h, rstd=rstd, eps=eps)
+        if not any(ctx.needs_input_grad):
+            codes = None
         # with codes an empty output: saved, it connects the gradients to x and residual, as h does where it is kept whole
         tie = None if codes is None else torch.empty(0, device=x.device)
         ctx.save_for_backward(gain, rstd, tie, *_keep(x if h is None else h, codes))
@@ -408,7 +416,7 @@ class RMSNorm(torch.nn.Module):
             raise ValueError("residual must have the shape and dtype of x")
         flat = lambda t: _packed(t.reshape(-1, self.width))  # noqa: E731
         y, _, *h = _RMSNorm.apply(flat(x), None if residual is None else flat(residual), _packed(self.gain), self.eps,
-                                  self.codes)
+                                  _codes_now(self))
         return y.view(x.shape) if residual is None else (y.view(x.shape), h[0].view(x.shape))
 
     def extra_repr(self) -> str:
