@@ -85,7 +85,8 @@ forge_status forge_grouped_gated(const forge_tensor* X, const forge_tensor* W, c
  * as the gradient of the stacked product: forge_grouped_dgrad of it with W gives dX, and
  * forge_grouped_wgrad or _step of X with it the weight's.  H (or NULL) is the input that the weight
  * gradient of the down projection takes.  The activations and their slopes are fp32 operations, whose
- * exponentials carry a rounding of their exponent x (g, g^2 / 2 for GELU): |x| 2^-23 of their value.
+ * exponentials carry a rounding of their exponent x (g, g^2 / 2 for GELU): |x| 2^-23 of their value.  Exponentials and
+ * act(g) / g below 2^-126 count as zero: act(g) of g below -87 (SiLU), -13.2 (GELU) or -10 (GELU_TANH).
  *
  * forge_gated_backward  dH [T, N], dgate_up [T, 2 N] and H [T, N] all F32 or all BF16; gate_up of the
  *   same dtype, or codes with scale [T, 2, ceil(N / 128)]: blocks begin anew at u.  Any N from 1 to

@@ -2,7 +2,8 @@
 //
 // The logistic function is 1 / (1 + 2^(-x log2 e)) by the hardware's exponential and reciprocal (one step
 // of fp32 each); the rounded exponent adds |x| 2^-24 of its value, which the 2^-9 of a bf16 result does
-// not show.  2^x runs into infinity and 1 / infinity is 0, so no |x| needs a branch.
+// not show.  2^x runs into infinity and 1 / infinity is 0, so no |x| needs a branch.  Neither instruction gives numbers
+// below 2^-126: there exponentials and logistic functions are 0.
 #pragma once
 
 #include "forge_ffn_internal.h"

@@ -5,11 +5,11 @@
 // gate rows of these columns and their 128 up rows, which is all that the products know of the
 // activation.  The epilogue is in forge_gated.h.
 //
-// 8192 rows by 14336 x 4096 with gate and up in e4m3: 1345-1375 us over the cards seen (1.40-1.43 PFLOP/s), 1283 without
-// them; the grouped product of the stacked weight alone takes 1272-1281.  The card's power bounds it: matrix cores 73 %
-// busy at 1.62 GHz.  16384 rows of 32 uneven experts by 1408 x 2048 with both in bf16: 195-211 us (0.90-0.97 PFLOP/s;
-// the grouped product alone 185-188), 43 % busy at 2.1 GHz: 902 tiles on 256 CUs, many of them of few rows.  One row by
-// 14336 x 4096: 48-54 us, 4.4-4.9 TB/s of weights.
+// 8192 rows by 14336 x 4096 with gate and up in e4m3: 1345-1412 us over the cards seen (1.36-1.43 PFLOP/s), 1283 without
+// them; the grouped product of the stacked weight alone takes 1272-1281.  The card's power bounds it: matrix cores 71 %
+// busy at 1.9 GHz.  16384 rows of 32 uneven experts by 1408 x 2048 with both in bf16: 195-211 us (0.90-0.97 PFLOP/s;
+// the grouped product alone 185-188), 43 % busy at 2.2 GHz: 902 tiles on 256 CUs, many of them of few rows.  One row by
+// 14336 x 4096: 48-56 us, 4.2-4.9 TB/s of weights.
 #include <hip/hip_runtime.h>
 
 #include "forge_gated.h"

@@ -3,10 +3,10 @@
 //     dg = dH u act'(g),  du = dH act(g),  H = act(g) u.
 // Without it dH would be written and read again, 4 bytes beside the 6 to 10 that an element cannot do without.
 //
-// 8192 rows by 14336 x 4096 from int8: 818-845 us over the cards seen (1.14-1.18 PFLOP/s and 0.95 GB; the grouped input gradient
+// 8192 rows by 14336 x 4096 from int8: 818-850 us over the cards seen (1.13-1.18 PFLOP/s and 0.95 GB; the grouped input gradient
 // and the activation's backward pass one after the other take 667 + 193, and 235 MB for dH).  Without its stores the
 // kernel takes 60 us less, without gate and up 65, without the activation 20.  16384 rows of 32 uneven experts by 1408 x
-// 2048 from bf16: 135-148 us (95 + 41 apart).  Tiles whose epilogues come at different times (every other CU, or XCD,
+// 2048 from bf16: 135-148 us; apart they take 95 + 41, no longer, but 46 MB for dH.  Tiles whose epilogues come at different times (every other CU, or XCD,
 // begins with half a tile) share less in L2: 826 -> 860 and 845 us.  Tiles of few rows or columns are not split further:
 // the last 256 tiles of a launch in two halves 145 -> 160 us for the experts.
 #include <hip/hip_runtime.h>
